@@ -271,13 +271,114 @@ int dense_swiglu_fp8(const void *x, const uint8_t *w13, const float *w13_s,
                      const uint8_t *w2, const float *w2_s, int d, int H, int T, void *y,
                      void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------- latent attention
+ *
+ * The attention half of the block ("Kimi-K2-Base", Attention; "Kimi K2 ·
+ * Architecture", config.json: kv_lora_rank 512, qk_rope_head_dim 64,
+ * qk_nope_head_dim 128, v_head_dim 128): keys and values of all heads come from one
+ * latent c of 512 columns and one rotary key of 64 columns per token.
+ *   expanded:  k_h = [W_uk,h c | k_pe],  v_h = W_uv,h c          (mla_attn_ragged)
+ *   absorbed:  q'_h = [W_uk,h^T q_nope,h | q_pe,h] against [c | k_pe], the output
+ *              W_uv,h o'_h with o'_h = sum_j p_j c_j              (mla_attn_paged)
+ * Both forms give the same attention. mla_head_proj computes the products with W_uk
+ * and W_uv; mla_rope_append makes the cache rows [c | k_pe].
+ *
+ * dtype MLA_BF16 or MLA_FP16 is the type of every 16-bit tensor of a call. Strides
+ * are in elements; the innermost dimension is contiguous; every stride is a positive
+ * multiple of 8 and every pointer 16-byte aligned (lse: 4-byte elements, contiguous).
+ * Products accumulate in fp32; softmax statistics and lse are fp32; results round once.
+ * Indices read on the device (slots, page tables, lengths) are checked there: a bad
+ * one sets bit 0x80 of the device error word (moe_check_device_error then returns
+ * MOE_ERR_INDEX) and its access is skipped. */
+#define MLA_BF16 0
+#define MLA_FP16 1
+
+/* Rotary frequencies for mla_rope_append, computed on the HOST in 64 bits:
+ * freq [dim/2] in units of 2^-64 turns per position, of f_i = base^(-2i/dim) / 2 pi.
+ * factor > 1 stretches them for long contexts (YaRN): with
+ *   pair(r) = dim ln(original_ctx / (2 pi r)) / (2 ln base),
+ *   low = max(floor(pair(beta_fast)), 0), high = min(ceil(pair(beta_slow)), dim - 1),
+ *   ramp_i = clamp((i - low) / max(high - low, 0.001), 0, 1),
+ * f_i becomes f_i (1 - ramp_i) + f_i / factor * ramp_i. dim even, in [2, 256];
+ * base > 1; factor >= 1 (1: original_ctx and the betas are not read). */
+int mla_rope_freqs(int dim, double base, double factor, int original_ctx, double beta_fast, double beta_slow,
+                   uint64_t *freq);
+
+/* Rotary positions, RMSNorm of the latent and the cache append, in one launch.
+ * q       [T, H, dim] at strides q_st, q_sh: the queries' rotary part, rotated into
+ *         q_out [T, H, dim] (qo_st, qo_sh); q_out may be q. q NULL: no queries.
+ * kv      [T, latent + dim] (row stride kv_st): each row's latent part becomes
+ *         c gamma / sqrt(mean(c^2) + eps) (gamma [latent]; NULL: copied as it is) and
+ *         its rotary part is rotated; the row is written to kv_out (kvo_st; may be kv
+ *         or NULL) and to the cache (may be NULL) at slots[t]: page slot / page_size,
+ *         row slot % page_size. A negative slot is not cached. Slots must be distinct.
+ *         kv NULL: only the queries.
+ * cache   [num_pages, page_size, latent + dim] (page_st, row_st)
+ * positions, slots [T] int32; freq [dim/2] on the device (mla_rope_freqs)
+ * layout  0: pairs (x_2i, x_2i+1); 1: pairs (x_i, x_i+dim/2)
+ * A pair (a, b) at angle t = 2 pi pos f_i becomes amplitude (a cos t - b sin t,
+ * b cos t + a sin t). dim % 16 == 0, dim <= 256; latent % 8 == 0, latent + dim <= 2048.
+ * The cache overlaps neither q nor kv. */
+int mla_rope_append(const void *q, int64_t q_st, int64_t q_sh, void *q_out, int64_t qo_st, int64_t qo_sh,
+                    const void *kv, int64_t kv_st, const void *gamma, float eps, void *kv_out, int64_t kvo_st,
+                    void *cache, int64_t page_st, int64_t row_st, int64_t num_pages, int page_size,
+                    const int32_t *slots, const int32_t *positions, const uint64_t *freq, float amplitude,
+                    int layout, int T, int H, int dim, int latent, int dtype, void *stream);
+
+/* Bytes of workspace for mla_attn_paged (any sizes) on the current device. */
+size_t mla_paged_workspace_bytes(void);
+
+/* Absorbed attention over the paged latent cache: the tokens of one decode step
+ * (cu_q NULL: sequence b's one query is row b) or chunks of new tokens (cu_q [B + 1]
+ * ascending from 0: rows cu_q[b] .. cu_q[b+1] - 1 are the last tokens of sequence b).
+ * The new tokens are already in the cache: query i of n sees the keys
+ * j < ctx[b] - n + i + 1. A query that sees none gives zeros and lse = -inf.
+ * q       [Tq, H, 576] (q_st, q_sh): the 512 latent columns, then the 64 rotary ones
+ * cache   [num_pages, page_size, 576] (page_st, row_st); page_size % 8 == 0
+ * table   [B, max_pages] int32 (row stride table_st): the pages of sequence b in order
+ * ctx     [B] int32: tokens of the sequence in the cache, the new ones included
+ * out     [Tq, H, 512] (o_st, o_sh); lse [Tq, H] fp32 natural log-sum-exp, or NULL
+ * 1 <= H <= 128; B <= 8192. Cache rows past a sequence's end may hold anything; a row
+ * that is some query's key is finite. Results do not depend on other sequences of the
+ * batch beyond the grouping of the fp32 sums; repeated calls give the same bits. */
+int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const void *cache, int64_t page_st,
+                   int64_t row_st, int64_t num_pages, int page_size, const int32_t *table, int64_t table_st,
+                   int max_pages, const int32_t *ctx, const int32_t *cu_q, int B, int H, float scale, int dtype,
+                   void *out, int64_t o_st, int64_t o_sh, float *lse, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/* Expanded attention of a ragged batch. Sequence b's queries are rows cu_q[b] ..
+ * cu_q[b+1] - 1 of q, its keys rows cu_k[b] .. cu_k[b+1] - 1 of k and v (both [B + 1]
+ * int32, ascending from 0). causal = 1: query i of n sees the keys j < c - n + i + 1 of
+ * the sequence's c; causal = 0: all c. A query that sees none gives zeros, lse = -inf.
+ * q       [Tq, H, 192] (q_st, q_sh): 128 columns, then the 64 rotary ones
+ * k_nope  [Tk, H, 128] (kn_st, kn_sh); k_pe [Tk, 64] (kp_st), shared by the heads
+ * v       [Tk, H, 128] (v_st, v_sh); k_nope and v may be views of one tensor
+ * out     [Tq, H, 128] (o_st, o_sh); lse [Tq, H] fp32 natural log-sum-exp, or NULL
+ * max_q   at least the longest sequence's queries (sizes the grid; a longer sequence
+ *         is reported as an index error and skipped). 1 <= H <= 1024; B <= 65535.
+ * Rows outside a sequence do not reach its results, whatever they hold. */
+int mla_attn_ragged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const void *k_nope, int64_t kn_st,
+                    int64_t kn_sh, const void *k_pe, int64_t kp_st, const void *v, int64_t v_st, int64_t v_sh,
+                    int64_t Tk, const int32_t *cu_q, const int32_t *cu_k, int B, int max_q, int H, float scale,
+                    int causal, int dtype, void *out, int64_t o_st, int64_t o_sh, float *lse, void *stream);
+
+/* Per-head projections out[t, h] = x[t, h] W_h.
+ * x       [T, H, K] (x_st, x_sh); x_shared = 1: [T, K] (x_st), the same for every head
+ * w       [H, N, K] (w_kn = 0) or [H, K, N] (w_kn = 1) at head stride w_sh, row stride w_sr
+ * out     [T, H, N] (o_st, o_sh), same dtype, fp32 accumulation
+ * K % 8 == 0, N % 8 == 0, both in [8, 8192]; 1 <= H <= 1024. */
+int mla_head_proj(const void *x, int64_t x_st, int64_t x_sh, int x_shared, const void *w, int64_t w_sh,
+                  int64_t w_sr, int w_kn, int T, int H, int K, int N, int dtype, void *out, int64_t o_st,
+                  int64_t o_sh, void *stream);
+
 /* Reads and clears the device error word of the current device after
  * synchronising `stream`. MOE_ERR_TIMEOUT if a kernel's bounded wait on an
  * mbarrier gave up since the last check (bits 0x01..0x10, 0x40; its outputs are
  * then invalid); otherwise MOE_ERR_INDEX if an index check failed and the
- * access was skipped (0x20: a GEMM work item outside the schedule; 0x80, the
- * bounds-checked build only: an expert id, a permuted position or an item's
- * rows outside their buffer); MOE_OK if no bit is set. *detail (may be NULL)
+ * access was skipped (0x20: a GEMM work item outside the schedule; 0x80: a slot,
+ * page, length or offset of the latent attention outside its buffer, and in the
+ * bounds-checked build an expert id, a permuted position or an item's rows); MOE_OK if no bit is set. *detail (may be NULL)
  * receives the raw error bits. */
 int moe_check_device_error(void *stream, uint32_t *detail);
 

@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe_fp8.so")
 MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_INDEX = 0, -1, -2, -3, -4, -5
 
 _c_int, _c_size, _c_i64, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_int64, ctypes.c_void_p
+_c_dbl = ctypes.c_double
 
 
 class MoeCfg(ctypes.Structure):
@@ -54,6 +55,19 @@ _SIGS = {
                                        ctypes.POINTER(MoeCfg), _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _c_size, _vp]),
     "dense_swiglu_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "dense_swiglu_fp8": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_size, _vp]),
+    "mla_rope_freqs": (_c_int, [_c_int, _c_dbl, _c_dbl, _c_int, _c_dbl, _c_dbl, _vp]),
+    "mla_rope_append": (_c_int, [_vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _vp, ctypes.c_float, _vp,
+                                 _c_i64, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp, _vp, _vp, ctypes.c_float, _c_int,
+                                 _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
+    "mla_paged_workspace_bytes": (_c_size, []),
+    "mla_attn_paged": (_c_int, [_vp, _c_i64, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _c_i64, _c_int, _vp, _c_i64, _c_int,
+                                _vp, _vp, _c_int, _c_int, ctypes.c_float, _c_int, _vp, _c_i64, _c_i64, _vp, _vp,
+                                _c_size, _vp]),
+    "mla_attn_ragged": (_c_int, [_vp, _c_i64, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_i64,
+                                 _c_i64, _vp, _vp, _c_int, _c_int, _c_int, ctypes.c_float, _c_int, _c_int, _vp,
+                                 _c_i64, _c_i64, _vp, _vp]),
+    "mla_head_proj": (_c_int, [_vp, _c_i64, _c_i64, _c_int, _vp, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int,
+                               _c_int, _c_int, _vp, _c_i64, _c_i64, _vp]),
     "moe_check_device_error": (_c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "moe_test_wait_timeout": (_c_int, [ctypes.c_uint64, _vp]),
     "moe_last_error_string": (ctypes.c_char_p, []),

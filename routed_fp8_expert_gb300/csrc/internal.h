@@ -1,6 +1,7 @@
 // Host-side interfaces shared by the library's translation units.
 #pragma once
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 #include <utility>
@@ -74,5 +75,9 @@ cudaError_t launch_combine_residual_rmsnorm(const void *o, const float *w, const
 // entry points defined in other translation units. report_error returns code.
 int report_error(int code, const char *msg);
 void report_launches(int n);
+
+// SMs of the current device; the driver's tensor-map encoder (NULL when it has none).
+int num_sms();
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 }  // namespace moe

@@ -1,0 +1,226 @@
+// Building blocks shared by the latent-attention kernels: the two 16-bit element
+// types, tcgen05 forms beyond those of ptx.cuh, and the launchers' argument blocks.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ptx.cuh"
+
+namespace moe {
+
+// The latent-attention shapes the tensor-core kernels are built for: a latent of 512
+// columns and a shared rotary key of 64 per token; heads of 128 + 64 (query, key) and
+// 128 (value) columns in the expanded form.
+constexpr int kMlaLatent = 512;
+constexpr int kMlaRope = 64;
+constexpr int kMlaWidth = kMlaLatent + kMlaRope;
+constexpr int kMlaNope = 128;
+constexpr int kMlaV = 128;
+
+template <typename T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+    static constexpr uint32_t kFmt = 1;   // kind::f16 operand format
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t u) {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
+    }
+    static __device__ __forceinline__ __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
+};
+template <> struct Elem<__half> {
+    static constexpr uint32_t kFmt = 0;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t u) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+    }
+    static __device__ __forceinline__ __half from(float v) { return __float2half_rn(v); }
+};
+
+// Instruction descriptor of kind::f16 with fp32 accumulation; a_mn / b_mn: the operand
+// is stored with its M (N) dimension contiguous instead of K.
+__host__ __device__ constexpr uint32_t idesc16(uint32_t fmt, int M, int N, bool a_mn = false, bool b_mn = false) {
+    return idesc_make(fmt, fmt, M, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+
+// Descriptor of an operand whose M (N) dimension is contiguous, stored as tiles of 64
+// columns: each K row is 128 bytes of one tile (128-byte swizzle, 8-row groups 1024
+// bytes apart) and consecutive tiles lie `tile_bytes` apart.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t tile_bytes) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((tile_bytes >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// D[tmem] (+)= A[tmem] B[smem], kind::f16.
+__device__ __forceinline__ void mma_16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+#define MLA_R8(b) "=r"(r[b]), "=r"(r[b + 1]), "=r"(r[b + 2]), "=r"(r[b + 3]), "=r"(r[b + 4]), "=r"(r[b + 5]), "=r"(r[b + 6]), "=r"(r[b + 7])
+#define MLA_W8(b) "r"(r[b]), "r"(r[b + 1]), "r"(r[b + 2]), "r"(r[b + 3]), "r"(r[b + 4]), "r"(r[b + 5]), "r"(r[b + 6]), "r"(r[b + 7])
+#define MLA_LIST32                                                                                                   \
+    "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29," \
+    "%30,%31}"
+#define MLA_LIST32_1                                                                                               \
+    "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29," \
+    "%30,%31,%32}"
+
+// 32 lanes x 32 consecutive columns: thread i gets lane (base + i).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " MLA_LIST32 ", [%32];"
+                 : MLA_R8(0), MLA_R8(8), MLA_R8(16), MLA_R8(24)
+                 : "r"(taddr));
+}
+
+// 16 lanes x 64 columns in the 16x256b shape: thread t gets, for every 8-column group
+// g, columns 8g + 2(t % 4) + {0, 1} of lane t / 4 (r[4g], r[4g + 1]) and of lane
+// t / 4 + 8 (r[4g + 2], r[4g + 3]).
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 " MLA_LIST32 ", [%32];"
+                 : MLA_R8(0), MLA_R8(8), MLA_R8(16), MLA_R8(24)
+                 : "r"(taddr));
+}
+
+// The store counterpart of tmem_ld32.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], " MLA_LIST32_1 ";" ::"r"(taddr), MLA_W8(0), MLA_W8(8),
+                 MLA_W8(16), MLA_W8(24)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Order this thread's generic-proxy shared-memory writes before later async-proxy
+// accesses (MMA operand reads, TMA) that are synchronised after it.
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// True for every thread of the named barrier when `p` holds for any of them.
+__device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\t"
+        "setp.ne.u32 a, %1, 0;\n\t"
+        "barrier.cta.red.or.pred b, %2, %3, a;\n\t"
+        "selp.u32 %0, 1, 0, b;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(p)), "r"(id), "r"(nthreads)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16-byte asynchronous global -> shared copy (bypassing L1).
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t dst, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_u32(uint32_t dst, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+}
+
+// Bounded wait of a whole role: false once any role of the CTA has given up.
+struct Waiter {
+    uint32_t abort_addr;
+    unsigned int *err;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, uint32_t bit) const {
+        return mbar_wait(bar, parity, abort_addr, err, bit);
+    }
+};
+
+// ---------------------------------------------------------------- argument blocks
+
+struct RopeArgs {
+    const void *q;            // [T, H, dim], strides below (elements)
+    int64_t q_st, q_sh;
+    void *q_out;
+    int64_t qo_st, qo_sh;
+    const void *kv;           // [T, latent + dim]
+    int64_t kv_st;
+    const void *gamma;        // [latent] or NULL
+    void *kv_out;             // or NULL
+    int64_t kvo_st;
+    void *cache;              // or NULL
+    int64_t page_st, row_st;
+    int64_t num_pages;
+    int page_size;
+    const int32_t *slots;
+    const int32_t *positions;
+    const uint64_t *freq;
+    int T, H, dim, latent, layout;
+    float amplitude, eps;
+    unsigned int *err;
+};
+
+struct PagedArgs {
+    const void *q;            // [Tq, H, 576]
+    int64_t q_st, q_sh;
+    int64_t Tq;
+    const int32_t *table;     // [B, table_st]
+    int64_t table_st;
+    const int32_t *ctx;       // [B]
+    const int32_t *cu_q;      // [B + 1] or NULL (one row each)
+    void *out;
+    int64_t o_st, o_sh;
+    float *lse;               // [Tq, H] or NULL
+    int64_t num_pages;
+    int max_pages, page_size, box_rows;
+    int B, H;
+    float scale_log2;         // scale * log2(e)
+    float *part_o;            // [2 * grid][64][512]
+    float2 *part_ml;          // [2 * grid][64]
+    int4 *joins;              // [grid]
+    unsigned int *err;
+};
+
+struct RaggedArgs {
+    const int32_t *cu_q, *cu_k;
+    int64_t Tq, Tk;
+    void *out;
+    int64_t o_st, o_sh;
+    float *lse;
+    int B, H, max_q, causal;
+    float scale_log2;
+    unsigned int *err;
+};
+
+struct ProjArgs {
+    void *out;
+    int64_t o_st, o_sh;
+    int T, H, K, N;
+    int shared_x;             // x has one head that every output head reads
+    unsigned int *err;
+};
+
+cudaError_t launch_rope(const RopeArgs &a, bool bf16, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged(const CUtensorMap &latent, const CUtensorMap &rope, const PagedArgs &a, bool bf16, int grid,
+                         cudaStream_t stream);
+cudaError_t launch_ragged(const CUtensorMap &q, const CUtensorMap &k_nope, const CUtensorMap &k_pe,
+                          const CUtensorMap &v, const RaggedArgs &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_proj(const CUtensorMap &x, const CUtensorMap &w, const ProjArgs &a, bool bf16, bool w_kn,
+                        int num_sms, cudaStream_t stream);
+
+}  // namespace moe

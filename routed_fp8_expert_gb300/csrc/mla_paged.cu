@@ -1,0 +1,688 @@
+// Absorbed latent attention over the paged cache (mla_attn_paged).
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "mla.cuh"
+
+namespace moe {
+
+namespace {
+
+// The (token, head) rows of a sequence are flattened (row = token * H + head) and cut
+// into tiles of 64; keys come in tiles of 64. For one pair of tiles
+//   S [64 rows, 64 keys]  = Q K^T          9 column groups of 64, M = 64, N = 64
+//   P = 2^(S scale - m)                     m: the row's reference maximum
+//   O^T [512, 64 rows]   += C^T P^T        4 blocks of 128 latent columns, M = 128, N = 64
+// The latent columns of the key tile serve both products from one copy in shared
+// memory: as B of the first (keys x columns, columns contiguous) and, transposed, as A
+// of the second. Holding O transposed keeps the accumulator at 256 of the 512 tensor
+// memory columns and lets every MMA of the larger product fill its 128 lanes, although
+// there are only 64 rows (one token of 64 heads). Q stays in shared memory (72 KB);
+// the key tiles pass through a ring of two (144 KB).
+//
+// One token of 64 heads does 121 flops per byte of cache: the HBM rate bounds it, and
+// the tensor work per tile (1,920 of the 3,100 cycles a tile takes to arrive) hides
+// behind the loads.
+//
+// The work is split evenly by key tiles over the CTAs, whatever the sequences' lengths:
+// the tiles of all (sequence, row tile) items form one line, CTA c takes the c-th part
+// of it, and an item that several CTAs share leaves partial sums that a second kernel
+// joins in a fixed order.
+constexpr int kRows = 64;
+constexpr int kKeys = 64;
+constexpr int kGroups = 4;                       // pairs of 64-column groups of the latent
+constexpr int kPairBytes = 2 * kKeys * 128;      // 16 KB
+constexpr int kGroupBytes = kKeys * 128;         // 8 KB
+constexpr int kPairSlots = 2 * kGroups;
+constexpr int kRopeSlots = 2;
+constexpr int kQBytes = (kMlaWidth / 64) * kRows * 128;
+constexpr int kOffP = kQBytes;
+constexpr int kOffPairs = kOffP + kRows * 128;
+constexpr int kOffRope = kOffPairs + kPairSlots * kPairBytes;
+constexpr int kOffMisc = kOffRope + kRopeSlots * kGroupBytes;
+constexpr int kSmem = kOffMisc + 2048;
+constexpr int kSoftWarps = 4;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kThreads = kSoftThreads + 64;      // + the loading warp and the MMA warp
+constexpr int kTmemO = 0;                        // 4 x 64 columns
+constexpr int kTmemS = 256;                      // 2 x 64 columns
+// A row's reference maximum follows its running maximum only when it falls behind by
+// more than 2^8: the sums then stay below 2^8 times their true scale, far from
+// overflow, and O is rescaled a few times per item instead of once per tile.
+constexpr float kLag = 8.0f;
+// Fewest key tiles a CTA is given: below it the partial sums cost more than the split gains.
+constexpr int kMinTiles = 2;
+
+static_assert(kQBytes >= 8192 * 8, "the start-up scan keeps one 8-byte prefix per sequence in the query buffer");
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+
+struct Shared {
+    uint64_t pair_full[kPairSlots], pair_empty[kPairSlots];
+    uint64_t rope_full[kRopeSlots], rope_empty[kRopeSlots];
+    uint64_t s_full[2], s_empty[2];
+    uint64_t p_full, pv_done, q_full, q_empty, mma_done;
+    uint32_t tmem;
+    int abort;
+    float factor[kRows];
+    int64_t row_off[kRows];
+    int64_t warp_sum[kThreads / 32];
+    int64_t total, lo, hi, start_off;
+    int start_b, parts;
+};
+static_assert(sizeof(Shared) <= 2048, "");
+
+// Queries and visible keys of sequence b. A length or offset outside its buffer is
+// recorded once and leaves the sequence without rows.
+struct Seq {
+    int row0, n, ctx;
+};
+__device__ __forceinline__ Seq read_seq(const PagedArgs &a, int b, bool report) {
+    Seq s;
+    s.ctx = a.ctx[b];
+    int64_t r0 = b, r1 = b + 1;
+    if (a.cu_q) r0 = a.cu_q[b], r1 = a.cu_q[b + 1];
+    const bool ok = r0 >= 0 && r1 >= r0 && r1 <= a.Tq && s.ctx >= 0 &&
+                    s.ctx <= static_cast<int64_t>(a.max_pages) * a.page_size;
+    if (!ok && report) record_error(a.err, ERR_BAD_INDEX);
+    s.row0 = ok ? static_cast<int>(r0) : 0;
+    s.n = ok ? static_cast<int>(r1 - r0) : 0;
+    if (!ok) s.ctx = 0;
+    return s;
+}
+
+__device__ __forceinline__ int row_tiles(const Seq &s, int H) {
+    return static_cast<int>((static_cast<int64_t>(s.n) * H + kRows - 1) / kRows);
+}
+
+// Keys that the last row of a row tile sees, and the key tiles that cover them (at
+// least one unit of work, so that rows without keys get their zeros).
+__device__ __forceinline__ int tile_keys(const Seq &s, int rt, int H) {
+    const int64_t last = min((static_cast<int64_t>(rt) + 1) * kRows, static_cast<int64_t>(s.n) * H) - 1;
+    const int64_t vis = static_cast<int64_t>(s.ctx) - s.n + last / H + 1;
+    return vis < 0 ? 0 : static_cast<int>(vis);
+}
+__device__ __forceinline__ int units_of(int keys) { return keys <= kKeys ? 1 : (keys - 1) / kKeys + 1; }
+
+// Walks a CTA's part [lo, hi) of the line of key tiles, item by item.
+struct Walk {
+    int b, rt, rts;
+    int64_t at, hi, off;   // off: units of item (b, rt) before `at`
+    Seq s;
+    // the current segment: key tiles [k0, k1) of `kt` of row tile rt of sequence b
+    int k0, k1, kt, keys;
+
+    __device__ void start(const PagedArgs &a, const Shared &sh) {
+        b = sh.start_b, rt = 0, at = sh.lo, hi = sh.hi, off = sh.start_off;
+        s = read_seq(a, b, false);
+        rts = row_tiles(s, a.H);
+    }
+    __device__ bool next(const PagedArgs &a) {
+        if (at >= hi) return false;
+        while (true) {
+            if (rt >= rts) {
+                ++b;
+                if (b >= a.B) return false;
+                rt = 0;
+                s = read_seq(a, b, false);
+                rts = row_tiles(s, a.H);
+                continue;
+            }
+            keys = tile_keys(s, rt, a.H);
+            const int u = units_of(keys);
+            if (off >= u) {
+                off -= u;
+                ++rt;
+                continue;
+            }
+            kt = u;
+            k0 = static_cast<int>(off);
+            const int64_t take = min(static_cast<int64_t>(u) - off, hi - at);
+            k1 = k0 + static_cast<int>(take);
+            return true;
+        }
+    }
+    __device__ void advance() {
+        at += k1 - k0;
+        off = 0;
+        ++rt;
+    }
+    // key tiles of the segment that hold keys
+    __device__ int tiles() const { return keys > 0 ? k1 - k0 : 0; }
+};
+
+__device__ __forceinline__ int64_t part_lo(int64_t total, int parts, int c) { return total * c / parts; }
+
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Every thread: the line's length, this CTA's part of it, and the sequence it starts in.
+__device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        Seq s{0, 0, 0};
+        if (b < a.B) s = read_seq(a, b, blockIdx.x == 0);
+        int64_t u = 0;
+        const int rts = row_tiles(s, a.H);
+        // few row tiles: one thread per sequence; many: the warp takes them together
+        if (rts <= 8)
+            for (int r = 0; r < rts; ++r) u += units_of(tile_keys(s, r, a.H));
+        unsigned many = __ballot_sync(0xffffffffu, rts > 8);
+        while (many) {
+            const int src = __ffs(many) - 1;
+            many &= many - 1;
+            Seq o;
+            o.row0 = 0;
+            o.n = __shfl_sync(0xffffffffu, s.n, src);
+            o.ctx = __shfl_sync(0xffffffffu, s.ctx, src);
+            const int orts = __shfl_sync(0xffffffffu, rts, src);
+            int64_t v = 0;
+            for (int r = lane; r < orts; r += 32) v += units_of(tile_keys(o, r, a.H));
+#pragma unroll
+            for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+            if (lane == src) u = v;
+        }
+        const int64_t inc = warp_scan(u, lane);
+        if (lane == 31) sh.warp_sum[warp] = inc;
+        __syncthreads();
+        int64_t before = base, all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sh.warp_sum[w];
+            all += sh.warp_sum[w];
+        }
+        if (b < a.B) prefix[b] = before + inc - u;
+        base += all;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        const int64_t most = (base + kMinTiles - 1) / kMinTiles;
+        const int parts = most < 1 ? 1 : most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+        const int c = blockIdx.x;
+        sh.total = base;
+        sh.parts = parts;
+        sh.lo = c < parts ? part_lo(base, parts, c) : base;
+        sh.hi = c < parts ? part_lo(base, parts, c + 1) : base;
+        sh.start_b = 0;
+        sh.start_off = 0;
+    }
+    __syncthreads();
+    if (sh.lo < sh.hi)
+        for (int b = tid; b < a.B; b += kThreads) {
+            const int64_t p = prefix[b], e = b + 1 < a.B ? prefix[b + 1] : sh.total;
+            if (p <= sh.lo && sh.lo < e) {
+                sh.start_b = b;
+                sh.start_off = sh.lo - p;
+            }
+        }
+    __syncthreads();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap map_lat, const __grid_constant__ CUtensorMap map_rope,
+                      const PagedArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem + kOffMisc);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    using E = Elem<T>;
+
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPairSlots; ++i) mbar_init(smem_u32(&sh.pair_full[i]), 1), mbar_init(smem_u32(&sh.pair_empty[i]), 1);
+        for (int i = 0; i < kRopeSlots; ++i) mbar_init(smem_u32(&sh.rope_full[i]), 1), mbar_init(smem_u32(&sh.rope_empty[i]), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.s_full[i]), 1), mbar_init(smem_u32(&sh.s_empty[i]), kSoftThreads);
+        mbar_init(smem_u32(&sh.p_full), kSoftThreads);
+        mbar_init(smem_u32(&sh.pv_done), 1);
+        mbar_init(smem_u32(&sh.q_full), kSoftThreads);
+        mbar_init(smem_u32(&sh.q_empty), 1);
+        mbar_init(smem_u32(&sh.mma_done), 1);
+        sh.abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&map_lat);
+        tma_prefetch_desc(&map_rope);
+    }
+    if (warp == kSoftWarps + 1) tmem_alloc<512>(smem_u32(&sh.tmem));
+    pdl_wait();
+    plan(a, sh, reinterpret_cast<int64_t *>(smem));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const Waiter wait{smem_u32(&sh.abort), a.err};
+
+    if (warp == kSoftWarps) {
+        // -------------------------------------------------------- loads
+        const uint64_t pol = policy_evict_first();
+        const int subs = kKeys / a.box_rows;   // boxes per key tile (one page each)
+        const int step = a.box_rows == 64 ? 2 : 1;
+        Walk w;
+        w.start(a, sh);
+        uint32_t tile = 0;
+        uint32_t used = 0, parity = 0;   // per slot (pairs, then rotary): loaded at all; last load's phase
+        bool ok = true;
+        while (ok && w.next(a)) {
+            const int n = w.tiles();
+            const int32_t *tab = a.table + static_cast<int64_t>(w.b) * a.table_st;
+            // the page of this lane's box, one tile ahead; a box past the last key reads
+            // zeros (its page lies past the cache)
+            auto page_of = [&](int k) -> int64_t {
+                const int64_t key = static_cast<int64_t>(k) * kKeys + lane * a.box_rows;
+                if (lane >= subs || key >= w.keys || k >= w.k1) return -1;
+                return tab[key / a.page_size];
+            };
+            int64_t page = page_of(w.k0);
+            for (int j = 0; j < n && ok; ++j, ++tile) {
+                const int k = w.k0 + j;
+                int64_t cur = page;
+                page = page_of(k + 1);
+                const int64_t key = static_cast<int64_t>(k) * kKeys + lane * a.box_rows;
+                const int row = static_cast<int>(key % a.page_size);
+                if (lane < subs && key < w.keys && (cur < 0 || cur >= a.num_pages)) {
+                    record_error(a.err, ERR_BAD_INDEX);
+                    cur = -1;
+                }
+                const int z = cur < 0 ? static_cast<int>(a.num_pages) : static_cast<int>(cur);
+                const uint32_t turn = tile >> 1;   // earlier uses of this half of the ring
+                for (int g = 0; g <= kGroups && ok; ++g) {
+                    const bool is_rope = g == kGroups;
+                    const int slot = is_rope ? tile & 1 : (tile & 1) * kGroups + g;
+                    const uint32_t full = smem_u32(is_rope ? &sh.rope_full[slot] : &sh.pair_full[slot]);
+                    const uint32_t empty = smem_u32(is_rope ? &sh.rope_empty[slot] : &sh.pair_empty[slot]);
+                    int got = 1;
+                    if (lane == 0) {
+                        got = wait(empty, (turn & 1) ^ 1, ERR_WAIT_SMEM_EMPTY);
+                        if (got) mbar_arrive_expect_tx(full, is_rope ? kGroupBytes : kPairBytes);
+                    }
+                    ok = __shfl_sync(0xffffffffu, got, 0);
+                    if (!ok) break;
+                    const int bit = is_rope ? kPairSlots + slot : slot;
+                    used |= 1u << bit;
+                    parity = (parity & ~(1u << bit)) | ((turn & 1) << bit);
+                    if (lane < subs) {
+                        const uint32_t dst = sbase + (is_rope ? kOffRope + slot * kGroupBytes : kOffPairs + slot * kPairBytes) +
+                                             lane * a.box_rows * 128;
+                        if (is_rope) {
+                            tma_load_4d(dst, &map_rope, full, 0, row, 2 * kGroups, z, pol);
+                        } else {
+                            for (int c = 0; c < 2; c += step)
+                                tma_load_4d(dst + c * kGroupBytes, &map_lat, full, 0, row, 2 * g + c, z, pol);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            w.advance();
+        }
+        // the ring's last loads must land before the CTA may exit
+        if (lane == 0)
+            for (int i = 0; i < kPairSlots + kRopeSlots; ++i)
+                if (used >> i & 1)
+                    mbar_wait_drain(smem_u32(i < kPairSlots ? &sh.pair_full[i] : &sh.rope_full[i - kPairSlots]),
+                                    parity >> i & 1, a.err);
+        __syncwarp();
+    } else if (warp == kSoftWarps + 1) {
+        // -------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc16(E::kFmt, kRows, kKeys);
+            constexpr uint32_t id_o = idesc16(E::kFmt, 128, kRows, true, false);
+            Walk w;
+            w.start(a, sh);
+            uint32_t s_tile = 0, p_tile = 0, seg = 0;
+            bool ok = true;
+            auto scores = [&](bool last) -> bool {
+                const uint32_t buf = s_tile & 1, ph = (s_tile >> 1) & 1;
+                if (!wait(smem_u32(&sh.s_empty[buf]), ph ^ 1, ERR_WAIT_PART_EMPTY)) return false;
+                const uint32_t d = tmem + kTmemS + buf * kKeys;
+                for (int g = 0; g <= kGroups; ++g) {
+                    const bool is_rope = g == kGroups;
+                    const int slot = is_rope ? buf : buf * kGroups + g;
+                    if (!wait(smem_u32(is_rope ? &sh.rope_full[slot] : &sh.pair_full[slot]), ph, ERR_WAIT_TMA_FULL)) return false;
+                    tc_fence_after();
+                    const uint32_t kb = sbase + (is_rope ? kOffRope + slot * kGroupBytes : kOffPairs + slot * kPairBytes);
+                    for (int c = 0; c < (is_rope ? 1 : 2); ++c)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(d, sdesc_sw128(sbase + (2 * g + c) * kRows * 128 + k * 32),
+                                     sdesc_sw128(kb + c * kGroupBytes + k * 32), id_s, g > 0 || c > 0 || k > 0);
+                }
+                mma_commit(smem_u32(&sh.s_full[buf]));
+                mma_commit(smem_u32(&sh.rope_empty[buf]));
+                if (last) mma_commit(smem_u32(&sh.q_empty));
+                ++s_tile;
+                return true;
+            };
+            while (ok && w.next(a)) {
+                const int n = w.tiles();
+                if (n > 0) {
+                    ok = wait(smem_u32(&sh.q_full), seg & 1, ERR_WAIT_TMA_FULL);
+                    ++seg;
+                    tc_fence_after();
+                    ok = ok && scores(n == 1);
+                    for (int j = 0; j < n && ok; ++j) {
+                        if (j + 1 < n && !scores(j + 2 == n)) { ok = false; break; }
+                        if (!wait(smem_u32(&sh.p_full), p_tile & 1, ERR_WAIT_PART_FULL)) { ok = false; break; }
+                        tc_fence_after();
+                        for (int g = 0; g < kGroups; ++g) {
+                            const int slot = (p_tile & 1) * kGroups + g;
+                            const uint32_t vb = sbase + kOffPairs + slot * kPairBytes;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16(tmem + kTmemO + g * kRows, sdesc_mn_sw128(vb + k * 2048, kGroupBytes),
+                                         sdesc_sw128(sbase + kOffP + k * 32), id_o, j > 0 || k > 0);
+                            mma_commit(smem_u32(&sh.pair_empty[slot]));
+                        }
+                        mma_commit(smem_u32(&sh.pv_done));
+                        ++p_tile;
+                    }
+                }
+                w.advance();
+            }
+            mma_commit(smem_u32(&sh.mma_done));
+            mbar_wait_drain(smem_u32(&sh.mma_done), 0, a.err);
+        }
+        __syncwarp();
+    } else {
+        // -------------------------------------------------------- softmax and results
+        const int tid = threadIdx.x;
+        const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+        // this thread's two rows of the tile and its 16 key columns (pairs of two)
+        const int ra = warp * 16 + lane / 4, rb = ra + 8;
+        const int c0 = 2 * (lane & 3);
+        Walk w;
+        w.start(a, sh);
+        uint32_t tile = 0, seg = 0;
+        int4 join = make_int4(-1, 0, 0, 0);
+        // after a wait that gave up a thread waits no more but keeps to the loops, so
+        // that every named barrier still gets all of its threads
+        bool ok = true;
+        auto hold = [&](uint64_t *bar, uint32_t parity, uint32_t bit) {
+            if (ok) ok = wait(smem_u32(bar), parity, bit);
+        };
+        while (w.next(a)) {
+            const int n = w.tiles();
+            const int64_t r0 = static_cast<int64_t>(w.rt) * kRows;
+            const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(w.s.n) * a.H - r0));
+            const bool whole = w.k0 == 0 && w.k1 == w.kt;
+            auto visible = [&](int r) {
+                if (r >= rows) return 0;
+                const int64_t v = static_cast<int64_t>(w.s.ctx) - w.s.n + (r0 + r) / a.H + 1;
+                return v < 0 ? 0 : static_cast<int>(v);
+            };
+            const int vis_a = visible(ra), vis_b = visible(rb);
+            float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
+            if (n > 0) {
+                // Q into shared memory (128-byte swizzle); rows past the sequence are zero
+                if (seg > 0) hold(&sh.q_empty, (seg - 1) & 1, ERR_WAIT_PART_EMPTY);
+                for (int i = tid; i < kRows * (kMlaWidth / 8); i += kSoftThreads) {
+                    const int r = i / (kMlaWidth / 8), v = i - r * (kMlaWidth / 8);
+                    const uint32_t dst = sbase + (v >> 3) * kRows * 128 + r * 128 + (((v & 7) ^ (r & 7)) << 4);
+                    if (r < rows) {
+                        const int64_t row = r0 + r, t = row / a.H, h = row - t * a.H;
+                        cp_async_16(dst, static_cast<const T *>(a.q) + (w.s.row0 + t) * a.q_st + h * a.q_sh + v * 8);
+                    } else {
+                        st_shared_v4(dst, make_uint4(0, 0, 0, 0));
+                    }
+                }
+                cp_async_wait_all();
+                fence_async_smem();
+                mbar_arrive(smem_u32(&sh.q_full));
+                ++seg;
+            }
+            for (int j = 0; j < n; ++j, ++tile) {
+                const uint32_t buf = tile & 1, ph = (tile >> 1) & 1;
+                hold(&sh.s_full[buf], ph, ERR_WAIT_PART_FULL);
+                tc_fence_after();
+                uint32_t r[32];
+                tmem_ld_16x64(tmem + kTmemS + buf * kKeys + lane_base, r);
+                tmem_wait_ld();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.s_empty[buf]));
+                const int kb = (w.k0 + j) * kKeys;
+                float mx_a = -INFINITY, mx_b = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = kb + 8 * g + c0 + e;
+                        const float sa = key < vis_a ? __uint_as_float(r[4 * g + e]) * a.scale_log2 : -INFINITY;
+                        const float sb = key < vis_b ? __uint_as_float(r[4 * g + 2 + e]) * a.scale_log2 : -INFINITY;
+                        r[4 * g + e] = __float_as_uint(sa);
+                        r[4 * g + 2 + e] = __float_as_uint(sb);
+                        mx_a = fmaxf(mx_a, sa);
+                        mx_b = fmaxf(mx_b, sb);
+                    }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, o));
+                    mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, o));
+                }
+                const bool behind = mx_a > m_a + kLag || mx_b > m_b + kLag;
+                if (named_bar_or(1, kSoftThreads, behind)) {
+                    const float na = fmaxf(m_a, mx_a), nb = fmaxf(m_b, mx_b);
+                    const float fa = m_a == -INFINITY ? 0.f : ex2(m_a - na), fb = m_b == -INFINITY ? 0.f : ex2(m_b - nb);
+                    l_a *= fa, l_b *= fb;
+                    m_a = na, m_b = nb;
+                    if (j > 0) {
+                        if ((lane & 3) == 0) sh.factor[ra] = fa, sh.factor[rb] = fb;
+                        hold(&sh.pv_done, (tile - 1) & 1, ERR_WAIT_PART_FULL);
+                        tc_fence_after();
+                        named_bar_sync(1, kSoftThreads);
+                        for (int c = 0; c < kGroups * kRows; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tmem + kTmemO + c + lane_base, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.factor[(c & 32) + i]);
+                            tmem_st32(tmem + kTmemO + c + lane_base, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const float ea = m_a == -INFINITY ? 0.f : m_a, eb = m_b == -INFINITY ? 0.f : m_b;
+                uint32_t pa[8], pb[8];
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const float a0 = ex2(__uint_as_float(r[4 * g]) - ea), a1 = ex2(__uint_as_float(r[4 * g + 1]) - ea);
+                    const float b0 = ex2(__uint_as_float(r[4 * g + 2]) - eb), b1 = ex2(__uint_as_float(r[4 * g + 3]) - eb);
+                    l_a += a0 + a1;
+                    l_b += b0 + b1;
+                    // the weights enter the second product in the tensors' 16-bit type:
+                    // half an ulp each, averaged over the keys
+                    pa[g] = E::pack(a0, a1);
+                    pb[g] = E::pack(b0, b1);
+                }
+                if (tile > 0) hold(&sh.pv_done, (tile - 1) & 1, ERR_WAIT_PART_FULL);
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    st_shared_u32(sbase + kOffP + ra * 128 + ((g ^ (ra & 7)) << 4) + c0 * 2, pa[g]);
+                    st_shared_u32(sbase + kOffP + rb * 128 + ((g ^ (rb & 7)) << 4) + c0 * 2, pb[g]);
+                }
+                // rows past the last key hold whatever the page held: their weights are
+                // zero, but zero times a NaN is not
+                const int left = w.keys - kb;
+                if (left < kKeys) {
+                    const uint32_t base = sbase + kOffPairs + (tile & 1) * kGroups * kPairBytes;
+                    const int per = (kKeys - left) * 8;   // 16-byte units per column group
+                    for (int i = tid; i < per * 2 * kGroups; i += kSoftThreads) {
+                        const int g = i / per;
+                        st_shared_v4(base + g * kGroupBytes + left * 128 + (i - g * per) * 16, make_uint4(0, 0, 0, 0));
+                    }
+                }
+                tc_fence_before();
+                fence_async_smem();
+                mbar_arrive(smem_u32(&sh.p_full));
+            }
+            // -------------------------------------------------- the segment's result
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                l_a += __shfl_xor_sync(0xffffffffu, l_a, o);
+                l_b += __shfl_xor_sync(0xffffffffu, l_b, o);
+            }
+            const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
+            named_bar_sync(1, kSoftThreads);   // factor and row_off are free again
+            if ((lane & 3) == 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = e ? rb : ra;
+                    const float l = e ? l_b : l_a, m = e ? m_b : m_a;
+                    const int64_t row = r0 + r, t = row / a.H, h = row - t * a.H;
+                    if (whole) {
+                        sh.factor[r] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+                        sh.row_off[r] = r < rows ? (w.s.row0 + t) * a.o_st + h * a.o_sh : -1;
+                        if (a.lse && r < rows)
+                            a.lse[(w.s.row0 + t) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                    } else if (r < rows) {
+                        a.part_ml[static_cast<int64_t>(slot) * kRows + r] = make_float2(m, l);
+                    }
+                }
+            }
+            named_bar_sync(1, kSoftThreads);
+            if (n > 0) {
+                hold(&sh.pv_done, (tile - 1) & 1, ERR_WAIT_PART_FULL);
+                tc_fence_after();
+            }
+            T *out = static_cast<T *>(a.out);
+            float *part = a.part_o + static_cast<int64_t>(slot) * kRows * kMlaLatent;
+            for (int c = 0; c < kGroups * kRows; c += 32) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(tmem + kTmemO + c + lane_base, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                }
+                const int dim = (c / kRows) * 128 + warp * 32 + lane;
+                const int rbase = c & 32;
+                if (whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int64_t off = sh.row_off[rbase + i];
+                        if (off >= 0) out[off + dim] = E::from(__uint_as_float(o[i]) * sh.factor[rbase + i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (rbase + i < rows) part[(rbase + i) * kMlaLatent + dim] = __uint_as_float(o[i]);
+                }
+            }
+            tc_fence_before();
+            if (!whole && w.k0 == 0) {
+                // this CTA holds the item's first key tiles: it names the item to the join
+                const int64_t last = w.at + (w.kt - 1);
+                int64_t c_end = blockIdx.x;
+                while (part_lo(sh.total, sh.parts, static_cast<int>(c_end) + 1) <= last) ++c_end;
+                join = make_int4(w.s.row0, static_cast<int>(r0), rows, static_cast<int>(c_end));
+                join.x = w.b;
+            }
+            w.advance();
+        }
+        if (tid == 0) a.joins[blockIdx.x] = join;
+    }
+    __syncthreads();
+    if (warp == kSoftWarps + 1) tmem_dealloc<512>(tmem);
+}
+
+// Joins the partial results of the items that several CTAs shared: row by row
+//   M = max m_s,  O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s
+// over the item's parts in order. joins[c] = (sequence, first row, rows, last CTA) of
+// the item whose first part CTA c holds (sequence -1: none). Four groups of 128
+// threads take every fourth part of a row, four columns each.
+constexpr int kJoinThreads = 512;
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs a, int ctas) {
+    __shared__ int4 s_join[256];
+    __shared__ float s_w[256];
+    __shared__ float4 s_acc[3][128];
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x;
+    for (int i = tid; i < ctas; i += kJoinThreads) s_join[i] = a.joins[i];
+    __syncthreads();
+    int first = 0;   // rows of the joins before join c
+    for (int c = 0; c < ctas; ++c) {
+        const int4 j = s_join[c];
+        if (j.x < 0) continue;
+        // rows of this join that fall to this block
+        int r = (static_cast<int>(blockIdx.x) - first) % static_cast<int>(gridDim.x);
+        if (r < 0) r += gridDim.x;
+        first += j.z;
+        for (; r < j.z; r += gridDim.x) {
+            const int parts = j.w - c + 1;
+            auto slot_of = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * kRows + r; };
+            float M = -INFINITY, L = 0.f;
+            __syncthreads();
+            if (tid < 32) {
+                for (int s = tid; s < parts; s += 32) M = fmaxf(M, a.part_ml[slot_of(s)].x);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                for (int s = tid; s < parts; s += 32) {
+                    const float2 ml = a.part_ml[slot_of(s)];
+                    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+                    s_w[s] = w;
+                    L += w * ml.y;
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+                __syncwarp();
+                const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);
+                for (int s = tid; s < parts; s += 32) s_w[s] *= inv;
+            }
+            __syncthreads();
+            const int grp = tid >> 7, col = tid & 127;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int s = grp; s < parts; s += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(a.part_o + slot_of(s) * kMlaLatent + col * 4);
+                const float w = s_w[s];
+                // a part without visible keys has weight zero and sums of zero
+                acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
+            }
+            if (grp > 0) s_acc[grp - 1][col] = acc;
+            __syncthreads();
+            if (grp == 0) {
+#pragma unroll
+                for (int g = 0; g < 3; ++g) {
+                    const float4 v = s_acc[g][col];
+                    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+                }
+                const Seq sq = read_seq(a, j.x, false);
+                const int64_t row = static_cast<int64_t>(j.y) + r, t = row / a.H, h = row - t * a.H;
+                T *dst = static_cast<T *>(a.out) + (sq.row0 + t) * a.o_st + h * a.o_sh + col * 4;
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(Elem<T>::pack(acc.x, acc.y), Elem<T>::pack(acc.z, acc.w));
+                if (a.lse && tid == 0)
+                    a.lse[(sq.row0 + t) * a.H + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+            }
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_t(const CUtensorMap &lat, const CUtensorMap &rope, const PagedArgs &a, int grid, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(paged_attn_kernel<T>, dim3(grid), dim3(kThreads), kSmem, stream, lat, rope, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_join_kernel<T>, dim3(2 * grid), dim3(kJoinThreads), 0, stream, a, grid);
+}
+
+}  // namespace
+
+cudaError_t launch_paged(const CUtensorMap &latent, const CUtensorMap &rope, const PagedArgs &a, bool bf16, int grid,
+                         cudaStream_t stream) {
+    if (grid > 256) return cudaErrorInvalidValue;   // the join keeps one entry per CTA in shared memory
+    return bf16 ? launch_t<__nv_bfloat16>(latent, rope, a, grid, stream)
+                : launch_t<__half>(latent, rope, a, grid, stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,338 @@
+// Expanded latent attention of a ragged batch (mla_attn_ragged).
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "mla.cuh"
+
+namespace moe {
+
+namespace {
+
+// One CTA takes 256 query rows of one head as two tiles of 128 and walks the sequence's
+// keys in tiles of 128 with the running maximum and sum of a softmax:
+//   S_t [128, 128]  = Q_t K^T      M = 128, N = 128, 192 columns (128 + the shared 64)
+//   P_t = 2^(S_t scale - m)
+//   O_t [128, 128] += P_t V        P_t in tensor memory, V with its columns contiguous
+// The two tiles alternate: while one's scores pass through the exponentials, the other's
+// products run. Both read one copy of the keys and values. K and V arrive in 16 KB
+// pieces (128 keys x 64 columns) through a ring of eight; the rotary piece is shared
+// by all heads, so the [k_nope | k_pe] concatenation is never stored.
+// Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each; P_t lies over the first half
+// of S_t (two 16-bit values per column). 2,560 tensor cycles per 256 x 128 scores
+// bound a long prompt.
+constexpr int kTile = 128;
+constexpr int kQRows = 2 * kTile;
+constexpr int kPiece = kTile * 128;              // 16 KB
+constexpr int kQPieces = 3;                      // per row tile
+constexpr int kSlots = 8;
+constexpr int kPerTile = 5;                      // 3 pieces of K, 2 of V
+constexpr int kOffRing = 2 * kQPieces * kPiece;
+constexpr int kOffMisc = kOffRing + kSlots * kPiece;
+constexpr int kSmem = kOffMisc + 1024;
+constexpr int kThreads = 2 * kTile + 64;         // a warpgroup per row tile, loads, MMA
+constexpr float kLag = 8.0f;                     // see mla_paged.cu
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+
+struct Shared {
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t q_full, s_full[2], p_full[2], o_full[2], mma_done;
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(Shared) <= 1024, "");
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    ragged_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kn,
+                       const __grid_constant__ CUtensorMap map_kp, const __grid_constant__ CUtensorMap map_v,
+                       const RaggedArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem + kOffMisc);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    using E = Elem<T>;
+
+    pdl_trigger();
+    pdl_wait();
+    // the longest rows first: they see the most keys
+    const int qt = gridDim.x - 1 - blockIdx.x;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1], kk0 = a.cu_k[b], kk1 = a.cu_k[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > a.Tq || kk0 < 0 || kk1 < kk0 || kk1 > a.Tk || q1 - q0 > a.max_q) {
+        if (threadIdx.x == 0 && qt == 0 && h == 0) record_error(a.err, ERR_BAD_INDEX);
+        return;
+    }
+    const int nq = static_cast<int>(q1 - q0), nk = static_cast<int>(kk1 - kk0);
+    const int r0 = qt * kQRows;
+    if (r0 >= nq) return;
+    const int rows = min(kQRows, nq - r0);
+    const bool two = rows > kTile;
+    // keys the CTA's last row sees
+    auto visible = [&](int row) {
+        if (!a.causal) return nk;
+        const int v = nk - nq + row + 1;
+        return v < 0 ? 0 : v;
+    };
+    const int keys = visible(r0 + rows - 1);
+    const int tiles = (keys + kTile - 1) / kTile;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(&sh.full[i]), 1), mbar_init(smem_u32(&sh.empty[i]), 1);
+        mbar_init(smem_u32(&sh.q_full), 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&sh.s_full[t]), 1);
+            mbar_init(smem_u32(&sh.p_full[t]), kTile);
+            mbar_init(smem_u32(&sh.o_full[t]), 1);
+        }
+        mbar_init(smem_u32(&sh.mma_done), 1);
+        sh.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) tmem_alloc<512>(smem_u32(&sh.tmem));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const Waiter wait{smem_u32(&sh.abort), a.err};
+
+    if (warp == 8) {
+        // -------------------------------------------------------- loads
+        if (lane == 0 && tiles > 0) {
+            const uint64_t pol = policy_evict_normal();
+            mbar_arrive_expect_tx(smem_u32(&sh.q_full), (two ? 2 : 1) * kQPieces * kPiece);
+            for (int t = 0; t < (two ? 2 : 1); ++t)
+                for (int c = 0; c < kQPieces; ++c)
+                    tma_load_3d(sbase + (t * kQPieces + c) * kPiece, &map_q, smem_u32(&sh.q_full), c * 64, h,
+                                static_cast<int>(q0) + r0 + t * kTile, pol);
+            uint32_t piece = 0, used = 0, parity = 0;
+            bool ok = true;
+            for (int j = 0; j < tiles && ok; ++j) {
+                const int key = static_cast<int>(kk0) + j * kTile;
+                for (int c = 0; c < kPerTile; ++c, ++piece) {
+                    const int slot = piece % kSlots;
+                    const uint32_t ph = (piece / kSlots) & 1;
+                    if (!wait(smem_u32(&sh.empty[slot]), ph ^ 1, ERR_WAIT_SMEM_EMPTY)) { ok = false; break; }
+                    const uint32_t full = smem_u32(&sh.full[slot]), dst = sbase + kOffRing + slot * kPiece;
+                    mbar_arrive_expect_tx(full, kPiece);
+                    if (c < 2) tma_load_3d(dst, &map_kn, full, c * 64, h, key, pol);
+                    else if (c == 2) tma_load_2d(dst, &map_kp, full, 0, key, pol);
+                    else tma_load_3d(dst, &map_v, full, (c - 3) * 64, h, key, pol);
+                    used |= 1u << slot;
+                    parity = (parity & ~(1u << slot)) | (ph << slot);
+                }
+            }
+            // the last loads must land before the CTA may exit
+            mbar_wait_drain(smem_u32(&sh.q_full), 0, a.err);
+            for (int i = 0; i < kSlots; ++i)
+                if (used >> i & 1) mbar_wait_drain(smem_u32(&sh.full[i]), parity >> i & 1, a.err);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // -------------------------------------------------------- MMA issue
+        if (lane == 0 && tiles > 0) {
+            constexpr uint32_t id_s = idesc16(E::kFmt, kTile, kTile);
+            constexpr uint32_t id_o = idesc16(E::kFmt, kTile, kMlaV, false, true);
+            constexpr uint32_t id_o64 = idesc16(E::kFmt, kTile, 64, false, true);
+            const int nt = two ? 2 : 1;
+            auto slot_of = [](uint32_t piece) { return piece % kSlots; };
+            auto arrived = [&](uint32_t piece) {
+                return wait(smem_u32(&sh.full[slot_of(piece)]), (piece / kSlots) & 1, ERR_WAIT_TMA_FULL);
+            };
+            // S_t of key tile j; the last row tile frees the pieces of K
+            auto scores = [&](int j, int t) -> bool {
+                for (int c = 0; c < 3; ++c) {
+                    const uint32_t piece = j * kPerTile + c;
+                    if (t == 0 && !arrived(piece)) return false;
+                    tc_fence_after();
+                    const uint32_t kb = sbase + kOffRing + slot_of(piece) * kPiece;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem + t * kTile, sdesc_sw128(sbase + (t * kQPieces + c) * kPiece + k * 32),
+                                 sdesc_sw128(kb + k * 32), id_s, c > 0 || k > 0);
+                    if (t == nt - 1) mma_commit(smem_u32(&sh.empty[slot_of(piece)]));
+                }
+                mma_commit(smem_u32(&sh.s_full[t]));
+                return true;
+            };
+            bool ok = wait(smem_u32(&sh.q_full), 0, ERR_WAIT_TMA_FULL);
+            for (int t = 0; t < nt && ok; ++t) ok = scores(0, t);
+            for (int j = 0; j < tiles && ok; ++j) {
+                const uint32_t v0 = j * kPerTile + 3;
+                const uint32_t s0 = slot_of(v0), s1 = slot_of(v0 + 1);
+                for (int t = 0; t < nt && ok; ++t) {
+                    // the values first: the warpgroup of row tile 0 clears rows past the end
+                    if (t == 0 && !(arrived(v0) && arrived(v0 + 1))) { ok = false; break; }
+                    if (!wait(smem_u32(&sh.p_full[t]), j & 1, ERR_WAIT_PART_FULL)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t p = tmem + t * kTile, o = tmem + 2 * kTile + t * kMlaV;
+                    const uint32_t b0 = sbase + kOffRing + s0 * kPiece, b1 = sbase + kOffRing + s1 * kPiece;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t acc = j > 0 || k > 0;
+                        if (s1 == s0 + 1) {
+                            mma_16_ts(o, p + k * 8, sdesc_mn_sw128(b0 + k * 2048, kPiece), id_o, acc);
+                        } else {   // the two pieces lie at the ring's end and start
+                            mma_16_ts(o, p + k * 8, sdesc_mn_sw128(b0 + k * 2048, kPiece), id_o64, acc);
+                            mma_16_ts(o + 64, p + k * 8, sdesc_mn_sw128(b1 + k * 2048, kPiece), id_o64, acc);
+                        }
+                    }
+                    if (t == nt - 1) {
+                        mma_commit(smem_u32(&sh.empty[s0]));
+                        mma_commit(smem_u32(&sh.empty[s1]));
+                    }
+                    if (j == tiles - 1) mma_commit(smem_u32(&sh.o_full[t]));
+                    // MMAs run in issue order: S_t of the next tile overwrites P_t after
+                    // the product above has read it
+                    if (j + 1 < tiles) ok = scores(j + 1, t);
+                }
+            }
+            mma_commit(smem_u32(&sh.mma_done));
+            mbar_wait_drain(smem_u32(&sh.mma_done), 0, a.err);
+        }
+        __syncwarp();
+    } else {
+        // -------------------------------------------------------- softmax and results
+        const int t = warp >> 2;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + t * kTile + lanes, to = tmem + 2 * kTile + t * kMlaV + lanes;
+        const int row = r0 + t * kTile + (warp & 3) * 32 + lane;
+        const bool valid = row < nq;
+        const int vis = valid ? visible(row) : 0;
+        // tiles that every row of the warp sees whole need no mask
+        const int vis_min = __reduce_min_sync(0xffffffffu, vis);
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        auto hold = [&](uint64_t *bar, uint32_t parity, uint32_t bit) {
+            if (ok) ok = wait(smem_u32(bar), parity, bit);
+        };
+        if (t == 0 || two) {
+            for (int j = 0; j < tiles; ++j) {
+                hold(&sh.s_full[t], j & 1, ERR_WAIT_PART_FULL);
+                __syncwarp();
+                tc_fence_after();
+                uint32_t r[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, r[c]);
+                tmem_wait_ld();
+                const int kb = j * kTile;
+                if (kb + kTile > vis_min) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (kb + c * 32 + i >= vis) r[c][i] = __float_as_uint(-INFINITY);
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[c][i]));
+                mx *= a.scale_log2;
+                const bool behind = mx > m + kLag;
+                if (__any_sync(0xffffffffu, behind)) {
+                    const float mn = fmaxf(m, mx);
+                    const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+                    l *= f;
+                    m = mn;
+                    if (j > 0) {
+                        // S_t of this tile was issued after P_t V of the one before, and
+                        // its completion covers both: O_t is at rest
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(to + c * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(to + c * 32, o);
+                        }
+                    }
+                }
+                const float e = m == -INFINITY ? 0.f : m;
+                uint32_t p[2][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float p0 = ex2(fmaf(__uint_as_float(r[c][i]), a.scale_log2, -e));
+                        const float p1 = ex2(fmaf(__uint_as_float(r[c][i + 1]), a.scale_log2, -e));
+                        l += p0 + p1;
+                        // the weights enter the second product in the tensors' 16-bit
+                        // type: half an ulp each, averaged over the keys
+                        p[c >> 1][(c & 1) * 16 + i / 2] = E::pack(p0, p1);
+                    }
+                    if (c & 1) tmem_st32(ts + (c >> 1) * 32, p[c >> 1]);
+                }
+                if (t == 0 && nk - kb < kTile) {
+                    // value rows past the sequence's end: their weights are zero, but
+                    // zero times a NaN is not. The rows are the next sequence's.
+                    const uint32_t v0 = j * kPerTile + 3;
+                    for (int c = 0; c < 2; ++c)
+                        hold(&sh.full[(v0 + c) % kSlots], ((v0 + c) / kSlots) & 1, ERR_WAIT_TMA_FULL);
+                    const int left = nk - kb, per = (kTile - left) * 8;
+                    for (int i = threadIdx.x; i < 2 * per; i += kTile) {
+                        const int c = i >= per;
+                        st_shared_v4(sbase + kOffRing + ((v0 + c) % kSlots) * kPiece + left * 128 + (i - c * per) * 16,
+                                     make_uint4(0, 0, 0, 0));
+                    }
+                    fence_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.p_full[t]));
+            }
+            if (tiles > 0) {
+                hold(&sh.o_full[t], 0, ERR_WAIT_PART_FULL);
+                __syncwarp();
+                tc_fence_after();
+            }
+            const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+            T *dst = static_cast<T *>(a.out) + (q0 + row) * a.o_st + h * a.o_sh;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                if (tiles > 0) {
+                    tmem_ld32(to + c * 32, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                }
+                if (valid) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = E::pack(__uint_as_float(o[i + 2 * k]) * inv, __uint_as_float(o[i + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(dst + c * 32 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (valid && a.lse)
+                a.lse[(q0 + row) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (warp == 9) tmem_dealloc<512>(tmem);
+}
+
+template <typename T>
+cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &kn, const CUtensorMap &kp, const CUtensorMap &v,
+                     const RaggedArgs &a, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(ragged_attn_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(ragged_attn_kernel<T>, dim3((a.max_q + kQRows - 1) / kQRows, a.H, a.B), dim3(kThreads), kSmem,
+                      stream, q, kn, kp, v, a);
+}
+
+}  // namespace
+
+cudaError_t launch_ragged(const CUtensorMap &q, const CUtensorMap &k_nope, const CUtensorMap &k_pe,
+                          const CUtensorMap &v, const RaggedArgs &a, bool bf16, cudaStream_t stream) {
+    return bf16 ? launch_t<__nv_bfloat16>(q, k_nope, k_pe, v, a, stream)
+                : launch_t<__half>(q, k_nope, k_pe, v, a, stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,427 @@
+"""The latent-attention operators against plain 64-bit forms, at the sizes and masks
+where they can go wrong."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import routed_fp8_expert_gb300 as moe
+from _mla_ref import attention, check, rope_frequencies, rotate, rounding
+from routed_fp8_expert_gb300 import _lib
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+SCALE = 192 ** -0.5
+BF16, FP16 = torch.bfloat16, torch.float16
+
+
+def randn(*shape, seed=0, dtype=BF16, std=1.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * std).to(dtype)
+
+
+def error_word():
+    detail = ctypes.c_uint32(0)
+    st = moe.load().moe_check_device_error(ctypes.c_void_p(torch.cuda.current_stream(DEV).cuda_stream),
+                                           ctypes.byref(detail))
+    return st, detail.value
+
+
+# ------------------------------------------------------------------ projections
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("w_kn", [False, True])
+@pytest.mark.parametrize("T,H,K,N,shared", [
+    (1, 1, 8, 8, False), (1, 64, 128, 512, False), (5, 3, 72, 40, False), (129, 5, 512, 128, False),
+    (300, 4, 512, 256, True), (64, 2, 136, 264, True), (257, 7, 128, 512, False),
+])
+def test_head_proj(T, H, K, N, shared, w_kn, dtype):
+    x = randn(T, 1 if shared else H, K, seed=T, dtype=dtype)
+    w = randn(*((H, K, N) if w_kn else (H, N, K)), seed=K, dtype=dtype, std=K ** -0.5)
+    y = moe.mla_head_proj(x.to(DEV), w.to(DEV), w_kn=w_kn)
+    assert error_word() == (_lib.MOE_OK, 0)
+    xd, wd = x.double().expand(T, H, K), w.double() if w_kn else w.double().transpose(1, 2)
+    ref = torch.einsum("thk,hkn->thn", xd, wd)
+    mag = torch.einsum("thk,hkn->thn", xd.abs(), wd.abs())
+    check(y, ref, rounding(dtype, ref) + (K / 16 + 8) * 2.0 ** -23 * mag, "out")
+
+
+def test_head_proj_reads_views_in_place():
+    # one up-projection weight [H, 256, 512] holds the key and the value halves of each
+    # head; the absorb product reads the key half with K contiguous rows swapped
+    H, T = 6, 19
+    w = randn(H, 256, 512, seed=1, std=0.05)
+    q = randn(T, H, 192, seed=2)
+    wd, qd = w.to(DEV), q.to(DEV)
+    out = torch.full((T, H, 576), 7.0, dtype=BF16, device=DEV)
+    moe.mla_head_proj(qd[..., :128], wd[:, :128], w_kn=True, out=out[..., :512])
+    ref = torch.einsum("thk,hkn->thn", q[..., :128].double(), w[:, :128].double())
+    mag = torch.einsum("thk,hkn->thn", q[..., :128].double().abs(), w[:, :128].double().abs())
+    check(out[..., :512], ref, rounding(BF16, ref) + 16 * 2.0 ** -23 * mag, "absorbed")
+    assert (out[..., 512:] == 7.0).all()                     # nothing written past the view
+    o = randn(T, H, 512, seed=3)
+    y = moe.mla_head_proj(o.to(DEV), wd[:, 128:])
+    ref = torch.einsum("thk,hnk->thn", o.double(), w[:, 128:].double())
+    mag = torch.einsum("thk,hnk->thn", o.double().abs(), w[:, 128:].double().abs())
+    check(y, ref, rounding(BF16, ref) + 40 * 2.0 ** -23 * mag, "value")
+
+
+# ------------------------------------------------------------------------ rope
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T,H,dim,latent,page,factor", [
+    (1, 1, 64, 512, 64, 1.0), (37, 64, 64, 512, 16, 32.0), (5, 3, 128, 256, 8, 4.0), (9, 20, 16, 8, 1, 1.0),
+    (3, 2, 256, 1792, 24, 40.0),
+])
+def test_rope_append(T, H, dim, latent, page, factor, layout, dtype):
+    g = torch.Generator().manual_seed(T)
+    plan = moe.rope_plan(dim, 50000.0, factor, mscale=1.0, mscale_all_dim=0.7, layout=layout, device=DEV)
+    amp = (1 + 0.1 * math.log(factor)) / (1 + 0.07 * math.log(factor))
+    assert abs(plan.amplitude - amp) < 1e-12
+    q = randn(T, H, 40 + dim, seed=T, dtype=dtype)           # the rotary part of wider heads
+    kv = randn(T, latent + dim, seed=T + 1, dtype=dtype, std=2.0)
+    gamma = (1 + 0.1 * torch.randn(latent, generator=g)).to(dtype)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, dtype=torch.int32)
+    pos[0] = 0
+    pages = (T + page - 1) // page + 2
+    cache = randn(pages, page, latent + dim, seed=5, dtype=dtype)
+    slots = torch.randperm(pages * page, generator=g)[:T].to(torch.int32)
+    if T > 2:
+        slots[1] = -1                                        # a padding token
+    cd = cache.to(DEV)
+    q_out, kv_out = moe.mla_rope_append(q.to(DEV)[..., 40:], kv.to(DEV), pos.to(DEV), plan, gamma=gamma.to(DEV),
+                                        cache=cd, slots=slots.to(DEV),
+                                        kv_out=torch.empty(T, latent + dim, dtype=dtype, device=DEV))
+    assert error_word() == (_lib.MOE_OK, 0)
+    freq = rope_frequencies(dim, 50000.0, factor)
+    ref, mag = rotate(q[..., 40:], pos, freq, layout, amp)
+    check(q_out, ref, rounding(dtype, ref) + 2.0 ** -20 * mag, "q")
+    c = kv[:, :latent].double()
+    c = c / torch.sqrt((c * c).mean(1, keepdim=True) + 1e-6) * gamma.double()
+    kr, kmag = rotate(kv[:, latent:], pos, freq, layout, amp)
+    row = torch.cat((c, kr), 1)
+    bound = rounding(dtype, row) + 2.0 ** -18 * torch.cat((c.abs(), kmag), 1)
+    check(kv_out, row, bound, "kv_out")
+    want = cache.clone()                                     # the cache holds kv_out's bits, and nothing else changed
+    for t, s in enumerate(slots.tolist()):
+        if s >= 0:
+            want[s // page, s % page] = kv_out[t].cpu()
+    assert torch.equal(cd.cpu(), want)
+
+
+def test_rope_in_place_and_alone():
+    T, H = 7, 4
+    plan = moe.rope_plan(64, device=DEV)
+    q, pos = randn(T, H, 192, seed=1).to(DEV), torch.arange(T, dtype=torch.int32, device=DEV)
+    want, _ = moe.mla_rope_append(q[..., 128:], None, pos, plan)
+    before = q.clone()
+    moe.mla_rope_append(q[..., 128:], None, pos, plan, q_out=q[..., 128:])
+    assert torch.equal(q[..., 128:], want) and torch.equal(q[..., :128], before[..., :128])
+    kv = randn(T, 576, seed=2).to(DEV)
+    _, out = moe.mla_rope_append(None, kv, pos, plan)        # no gamma: the latent is copied
+    assert torch.equal(out[:, :512], kv[:, :512])
+    none, _ = moe.mla_rope_append(q[:0, :, 128:], None, pos[:0], plan)
+    assert none.shape == (0, H, 64)
+
+
+def test_rope_bad_slot_is_skipped_and_reported():
+    plan = moe.rope_plan(64, device=DEV)
+    kv, cache = randn(3, 576, seed=1).to(DEV), torch.zeros(2, 8, 576, dtype=BF16, device=DEV)
+    pos = torch.arange(3, dtype=torch.int32, device=DEV)
+    slots = torch.tensor([3, 16, -5], dtype=torch.int32, device=DEV)
+    moe.mla_rope_append(None, kv, pos, plan, cache=cache, slots=slots)
+    assert error_word() == (_lib.MOE_ERR_INDEX, 0x80)
+    assert error_word() == (_lib.MOE_OK, 0)
+    flat = cache.view(16, 576)
+    assert (flat[3] != 0).any() and flat.abs().sum() == flat[3].abs().sum()
+
+
+def test_rope_of_a_strided_multi_layer_cache():
+    layers, page = 3, 16
+    plan = moe.rope_plan(64, device=DEV)
+    big = torch.zeros(4, layers, page, 576, dtype=BF16, device=DEV)
+    kv, pos = randn(20, 576, seed=4).to(DEV), torch.arange(20, dtype=torch.int32, device=DEV)
+    _, rows = moe.mla_rope_append(None, kv, pos, plan)
+    moe.mla_rope_append(None, kv, pos, plan, cache=big[:, 1], slots=pos + 7)
+    flat = big[:, 1].reshape(-1, 576)
+    assert torch.equal(flat[7:27], rows)
+    assert (big[:, 0] == 0).all() and (big[:, 2] == 0).all() and (flat[:7] == 0).all() and (flat[27:] == 0).all()
+
+
+# ----------------------------------------------------------------------- paged
+
+def paged_inputs(ctx, n, H, page, seed=0, dtype=BF16, std=1.0, junk=None, extra_cols=3):
+    """A cache whose pages are shuffled; page rows past a sequence's end (and unused
+    pages) hold `junk`."""
+    g = torch.Generator().manual_seed(seed)
+    need = [(c + page - 1) // page for c in ctx]
+    total = sum(need) + 2
+    perm = torch.randperm(total, generator=g)
+    cache = randn(total, page, 576, seed=seed, dtype=dtype, std=std)
+    table = torch.full((len(ctx), max(need + [1]) + extra_cols), 2 ** 30, dtype=torch.int32)   # unused entries: not a page
+    at, used = 0, torch.zeros(total, page, dtype=torch.bool)
+    for b, (c, k) in enumerate(zip(ctx, need)):
+        pages = perm[at:at + k]
+        table[b, :k] = pages.to(torch.int32)
+        at += k
+        for i in range(k):
+            used[pages[i], :min(page, c - i * page)] = True
+    if junk is not None:
+        cache[~used] = junk
+    q = randn(sum(n), H, 576, seed=seed + 1, dtype=dtype)
+    return q, cache, table, torch.tensor(ctx, dtype=torch.int32)
+
+
+def paged_ref(q, cache, table, ctx, n, dtype, scale=SCALE):
+    outs, at = [], 0
+    page, H = cache.shape[1], q.shape[1]
+    for b, c in enumerate(ctx.tolist()):
+        keys = torch.cat([cache[p] for p in table[b, :(c + page - 1) // page].tolist()] + [cache[:0, 0]])[:c]
+        rows = q[at:at + n[b]].reshape(-1, 576)
+        vis = [max(0, c - n[b] + i + 1) for i in range(n[b]) for _ in range(H)]
+        outs.append(attention(rows, keys, keys[:, :512], vis, scale, dtype))
+        at += n[b]
+    o, lse, ob, lb = (torch.cat(x) for x in zip(*outs))
+    return o.view(at, H, 512), lse.view(at, H), ob.view(at, H, 512), lb.view(at, H)
+
+
+def run_paged(q, cache, table, ctx, n, **kw):
+    cu = None
+    if any(x != 1 for x in n):
+        cu = torch.tensor([0] + n, dtype=torch.int32).cumsum(0).to(torch.int32).to(DEV)
+    return moe.mla_attn_paged(q.to(DEV), cache.to(DEV), table.to(DEV), ctx.to(DEV), SCALE, cu_q=cu, want_lse=True, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("ctx,n,H,page", [
+    ([1], [1], 64, 64), ([64], [1], 64, 64), ([65], [1], 16, 64), ([0], [1], 64, 64),
+    ([130, 0, 1, 63, 1000], [1] * 5, 64, 64), ([257, 700], [1, 1], 128, 32), ([5, 77, 300], [1] * 3, 1, 8),
+    ([333, 90], [1, 1], 20, 24), ([40, 129, 128], [4, 4, 1], 16, 16), ([3, 200], [5, 70], 20, 128),
+    ([100, 10], [100, 10], 7, 64), ([1500], [3], 64, 192), ([50, 60], [0, 2], 64, 64),
+])
+def test_paged(ctx, n, H, page, dtype):
+    q, cache, table, ctx_t = paged_inputs(ctx, n, H, page, seed=sum(ctx) + H, dtype=dtype, junk=math.nan)
+    o, lse = run_paged(q, cache, table, ctx_t, n)
+    assert error_word() == (_lib.MOE_OK, 0)
+    ro, rl, ob, lb = paged_ref(q, cache, table, ctx_t, n, dtype)
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
+
+
+@pytest.mark.parametrize("junk", [math.inf, -math.inf, torch.finfo(BF16).max])
+def test_paged_stale_rows_do_not_count(junk):
+    ctx, n = [70, 1, 128, 190], [1] * 4
+    q, cache, table, ctx_t = paged_inputs(ctx, n, 64, 64, seed=3, junk=junk)
+    o, lse = run_paged(q, cache, table, ctx_t, n)
+    ro, rl, ob, lb = paged_ref(q, cache, table, ctx_t, n, BF16)
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
+
+
+def test_paged_rising_scores_move_the_reference_maximum():
+    # scores that grow along the keys: the running maximum rises by far more than the
+    # lag in every tile; then scores of the lowest magnitude
+    L = 900
+    q, cache, table, ctx_t = paged_inputs([L], [1], 64, 64, seed=8)
+    page = 64
+    for i, p in enumerate(table[0, :(L + 63) // 64].tolist()):
+        cache[p] = cache[p] * 0.1
+        cache[p, :, 0] = (torch.arange(page) + i * page).to(BF16)
+    q[..., 0] = 4.0
+    o, lse = run_paged(q, cache, table, ctx_t, [1])
+    ro, rl, ob, lb = paged_ref(q, cache, table, ctx_t, [1], BF16)
+    check(o, ro, ob, "rising out")
+    check(lse, rl, lb, "rising lse")
+    q[..., 0] = -4.0
+    o, lse = run_paged(q, cache, table, ctx_t, [1])
+    ro, rl, ob, lb = paged_ref(q, cache, table, ctx_t, [1], BF16)
+    check(o, ro, ob, "falling out")
+    check(lse, rl, lb, "falling lse")
+
+
+def test_paged_long_context_is_split_and_joined():
+    ctx, n = [20000, 3, 9000], [1, 1, 2]
+    q, cache, table, ctx_t = paged_inputs(ctx, n, 16, 64, seed=9)
+    o, lse = run_paged(q, cache, table, ctx_t, n)
+    ro, rl, ob, lb = paged_ref(q, cache, table, ctx_t, n, BF16)
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
+    o2, lse2 = run_paged(q, cache, table, ctx_t, n)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)     # the same bits again
+
+
+def test_paged_views_and_strides():
+    ctx, n, H = [150, 90], [1, 1], 8
+    q, cache, table, ctx_t = paged_inputs(ctx, n, H, 32, seed=11)
+    base, lse0 = run_paged(q, cache, table, ctx_t, n)
+    wide_q = torch.zeros(2, H, 640, dtype=BF16)
+    wide_q[..., 32:608] = q
+    big = torch.full((cache.shape[0], 2, 32, 584), math.nan, dtype=BF16)
+    big[:, 1, :, :576] = cache
+    out = torch.full((H, 2, 520), 5.0, dtype=BF16, device=DEV)
+    got, lse = moe.mla_attn_paged(wide_q.to(DEV)[..., 32:608], big.to(DEV)[:, 1, :, :576], table.to(DEV), ctx_t.to(DEV),
+                                  SCALE, out=out.transpose(0, 1)[..., :512], want_lse=True)
+    assert torch.equal(got, base) and torch.equal(lse, lse0) and (out[..., 512:] == 5.0).all()
+
+
+def test_paged_many_sequences():
+    # more sequences than the start-up scan takes at once
+    ctx = [(37 * i) % 150 for i in range(500)]
+    n = [1] * 500
+    q, cache, table, ctx_t = paged_inputs(ctx, n, 4, 16, seed=2)
+    o, lse = run_paged(q, cache, table, ctx_t, n)
+    ro, rl, ob, lb = paged_ref(q, cache, table, ctx_t, n, BF16)
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
+
+
+def test_paged_bad_indices_are_reported_and_skipped():
+    q, cache, table, ctx_t = paged_inputs([100, 100], [1, 1], 64, 64, seed=5)
+    good, _ = run_paged(q, cache, table, ctx_t, [1, 1])
+    bad = table.clone()
+    bad[1, 1] = cache.shape[0]                               # a page past the cache
+    o, _ = run_paged(q, cache, bad, ctx_t, [1, 1])
+    assert error_word() == (_lib.MOE_ERR_INDEX, 0x80)
+    assert torch.equal(o[0], good[0])
+    long = ctx_t.clone()
+    long[1] = table.shape[1] * 64 + 1                        # more tokens than its table holds
+    out = torch.full_like(good, 3.0)
+    moe.mla_attn_paged(q.to(DEV), cache.to(DEV), table.to(DEV), long.to(DEV), SCALE, out=out)
+    assert error_word() == (_lib.MOE_ERR_INDEX, 0x80)
+    assert torch.equal(out[0], good[0]) and (out[1] == 3.0).all()
+    cu = torch.tensor([0, 1, 3], dtype=torch.int32, device=DEV)   # past the two rows of q
+    out = torch.full_like(good, 3.0)
+    moe.mla_attn_paged(q.to(DEV), cache.to(DEV), table.to(DEV), ctx_t.to(DEV), SCALE, cu_q=cu, out=out)
+    assert error_word() == (_lib.MOE_ERR_INDEX, 0x80)
+    assert torch.equal(out[0], good[0]) and (out[1] == 3.0).all()
+    assert error_word() == (_lib.MOE_OK, 0)
+
+
+def test_paged_in_a_graph_follows_new_lengths():
+    ctx, n = [90, 700], [1, 1]
+    q, cache, table, ctx_t = paged_inputs([200, 800], n, 64, 64, seed=6)
+    qd, cd, td, ld = q.to(DEV), cache.to(DEV), table.to(DEV), torch.tensor(ctx, dtype=torch.int32, device=DEV)
+    ws, out = moe.mla_paged_workspace(DEV), torch.empty(2, 64, 512, dtype=BF16, device=DEV)
+    moe.mla_attn_paged(qd, cd, td, ld, SCALE, out=out, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.mla_attn_paged(qd, cd, td, ld, SCALE, out=out, ws=ws)
+    for lens in ([90, 700], [200, 0], [1, 800]):
+        ld.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, moe.mla_attn_paged(qd, cd, td, ld, SCALE, ws=ws))
+
+
+# ---------------------------------------------------------------------- ragged
+
+def ragged_ref(q, kn, kp, v, nq, nk, causal, dtype):
+    outs, qa, ka = [], 0, 0
+    H = q.shape[1]
+    for n, c in zip(nq, nk):
+        per = []
+        for h in range(H):
+            k = torch.cat((kn[ka:ka + c, h], kp[ka:ka + c]), 1)
+            vis = [max(0, c - n + i + 1) if causal else c for i in range(n)]
+            per.append(attention(q[qa:qa + n, h], k, v[ka:ka + c, h], vis, SCALE, dtype))
+        outs.append([torch.stack(x, 1) for x in zip(*per)])
+        qa, ka = qa + n, ka + c
+    return [torch.cat(x) for x in zip(*outs)]
+
+
+def offsets(lens):
+    return torch.tensor([0] + list(lens), dtype=torch.int32).cumsum(0).to(torch.int32).to(DEV)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("nq,nk,H", [
+    ([1], [1], 1), ([128], [128], 2), ([129], [129], 1), ([300], [300], 2), ([1, 0, 260, 17], [1, 5, 260, 400], 3),
+    ([64, 3], [0, 2], 2), ([40], [700], 2), ([513], [200], 1), ([5, 5, 5], [130, 128, 127], 8),
+])
+def test_ragged(nq, nk, H, causal, dtype):
+    s = sum(nq) + 7 * H
+    q = randn(sum(nq), H, 192, seed=s, dtype=dtype)
+    kv = randn(sum(nk) + 3, H, 256, seed=s + 1, dtype=dtype)
+    kp = randn(sum(nk) + 3, 64, seed=s + 2, dtype=dtype)
+    kv[sum(nk):], kp[sum(nk):] = math.nan, math.nan          # rows past every sequence
+    kvd = kv.to(DEV)
+    o, lse = moe.mla_attn_ragged(q.to(DEV), kvd[..., :128], kp.to(DEV), kvd[..., 128:], offsets(nq), offsets(nk),
+                                 max(nq), SCALE, causal=causal, want_lse=True)
+    assert error_word() == (_lib.MOE_OK, 0)
+    ro, rl, ob, lb = ragged_ref(q, kv[..., :128], kp, kv[..., 128:], nq, nk, causal, dtype)
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
+
+
+def test_ragged_neighbours_do_not_leak():
+    # the sequence between two of NaN and infinity
+    nq = nk = [70, 200, 90]
+    H = 2
+    q, kv, kp = randn(360, H, 192, seed=1), randn(360, H, 256, seed=2), randn(360, 64, seed=3)
+    clean = [x.clone() for x in (q, kv, kp)]
+    for x, bad in ((q, math.nan), (kv, math.inf), (kp, math.nan)):
+        x[:70], x[270:] = bad, bad
+    kvd = kv.to(DEV)
+    o, lse = moe.mla_attn_ragged(q.to(DEV), kvd[..., :128], kp.to(DEV), kvd[..., 128:], offsets(nq), offsets(nk), 200,
+                                 SCALE, want_lse=True)
+    ro, rl, ob, lb = ragged_ref(clean[0], clean[1][..., :128], clean[2], clean[1][..., 128:], nq, nk, True, BF16)
+    check(o[70:270], ro[70:270], ob[70:270], "out")
+    check(lse[70:270], rl[70:270], lb[70:270], "lse")
+
+
+def test_ragged_rising_scores_move_the_reference_maximum():
+    n = 640
+    q, kv, kp = randn(n, 1, 192, seed=1) * 0.1, randn(n, 1, 256, seed=2), randn(n, 64, seed=3) * 0.1
+    kp[:, 0], q[..., 128] = torch.arange(n).to(BF16), 4.0
+    for sign in (1, -1):
+        kvd = kv.to(DEV)
+        o, lse = moe.mla_attn_ragged((q * sign).to(DEV), kvd[..., :128], kp.to(DEV), kvd[..., 128:], offsets([n]),
+                                     offsets([n]), n, SCALE, want_lse=True)
+        ro, rl, ob, lb = ragged_ref(q * sign, kv[..., :128], kp, kv[..., 128:], [n], [n], True, BF16)
+        check(o, ro, ob, "out")
+        check(lse, rl, lb, "lse")
+
+
+def test_ragged_strides_and_output_view():
+    n, H = 140, 4
+    q, kv, kp = randn(n, H, 192, seed=4).to(DEV), randn(n, H, 256, seed=5).to(DEV), randn(n, 64, seed=6).to(DEV)
+    cu = offsets([100, 40])
+    base = moe.mla_attn_ragged(q, kv[..., :128], kp, kv[..., 128:], cu, cu, 100, SCALE)
+    qh = q.transpose(0, 1).contiguous().transpose(0, 1)      # heads outermost
+    kh = kv[..., :128].transpose(0, 1).contiguous().transpose(0, 1)
+    wide = torch.zeros(n, 96, dtype=BF16, device=DEV)
+    wide[:, 16:80] = kp
+    out = torch.full((H, n, 136), 9.0, dtype=BF16, device=DEV)
+    got = moe.mla_attn_ragged(qh, kh, wide[:, 16:80], kv[..., 128:], cu, cu, 100, SCALE,
+                              out=out.transpose(0, 1)[..., :128])
+    assert torch.equal(got, base) and (out[..., 128:] == 9.0).all()
+
+
+def test_ragged_bad_offsets_are_reported_and_skipped():
+    q, kv, kp = randn(20, 1, 192).to(DEV), randn(20, 1, 256).to(DEV), randn(20, 64).to(DEV)
+    for cu, max_q in (([0, 21], 30), ([0, 20], 10), ([-1, 20], 30), ([5, 2], 30)):
+        cu_t = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        out = torch.full((20, 1, 128), 3.0, dtype=BF16, device=DEV)
+        moe.mla_attn_ragged(q, kv[..., :128], kp, kv[..., 128:], cu_t, cu_t, max_q, SCALE, out=out)
+        assert error_word() == (_lib.MOE_ERR_INDEX, 0x80)
+        assert (out == 3.0).all()
+
+
+# ------------------------------------------------------------- streams, both forms
+
+def test_on_another_stream():
+    q, kv, kp = randn(50, 2, 192).to(DEV), randn(50, 2, 256).to(DEV), randn(50, 64).to(DEV)
+    cu = offsets([50])
+    want = moe.mla_attn_ragged(q, kv[..., :128], kp, kv[..., 128:], cu, cu, 50, SCALE)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(DEV)
+    with torch.cuda.stream(s):
+        late = q * 0
+        late += q                                            # q is produced on this stream
+        got = moe.mla_attn_ragged(late, kv[..., :128], kp, kv[..., 128:], cu, cu, 50, SCALE)
+    s.synchronize()
+    assert torch.equal(got, want)

@@ -1,0 +1,121 @@
+"""Latent attention on the host: rotary frequencies and the refusals of every call.
+No GPU: bad arguments are turned away before anything is enqueued."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import routed_fp8_expert_gb300 as moe
+from _mla_ref import rope_frequencies
+from routed_fp8_expert_gb300 import _lib, build
+
+P = ctypes.c_void_p(0x1000)
+ODD = ctypes.c_void_p(0x1008)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+@pytest.mark.parametrize("dim,base,kw", [
+    (64, 10000.0, {}), (64, 50000.0, dict(factor=32.0)), (128, 500000.0, dict(factor=8.0, original_ctx=8192)),
+    (2, 10000.0, {}), (64, 50000.0, dict(factor=32.0, beta_fast=1.0, beta_slow=1.0)), (256, 1.5, dict(factor=2.0)),
+])
+def test_rope_frequencies(lib, dim, base, kw):
+    f = (ctypes.c_uint64 * (dim // 2))()
+    assert lib.mla_rope_freqs(dim, base, kw.get("factor", 1.0), kw.get("original_ctx", 4096),
+                              kw.get("beta_fast", 32.0), kw.get("beta_slow", 1.0), f) == _lib.MOE_OK
+    want = rope_frequencies(dim, base, **kw) / (2 * math.pi)
+    got = torch.tensor([v / 2.0 ** 64 for v in f], dtype=torch.float64)
+    assert torch.allclose(got, want, rtol=1e-14, atol=2.0 ** -63)
+
+
+@pytest.mark.parametrize("args,code", [
+    ((63, 1e4, 1.0, 4096, 32.0, 1.0), _lib.MOE_ERR_UNSUPPORTED), ((258, 1e4, 1.0, 4096, 32.0, 1.0), _lib.MOE_ERR_UNSUPPORTED),
+    ((0, 1e4, 1.0, 4096, 32.0, 1.0), _lib.MOE_ERR_UNSUPPORTED), ((64, 1.0, 1.0, 4096, 32.0, 1.0), _lib.MOE_ERR_ARG),
+    ((64, math.nan, 1.0, 4096, 32.0, 1.0), _lib.MOE_ERR_ARG), ((64, 1e4, 0.5, 4096, 32.0, 1.0), _lib.MOE_ERR_ARG),
+    ((64, 1e4, 2.0, 0, 32.0, 1.0), _lib.MOE_ERR_ARG), ((64, 1e4, 2.0, 4096, 0.0, 1.0), _lib.MOE_ERR_ARG),
+    ((64, 1e4, 2.0, 4096, 32.0, math.inf), _lib.MOE_ERR_ARG),
+])
+def test_rope_frequencies_refused(lib, args, code):
+    assert lib.mla_rope_freqs(*args, (ctypes.c_uint64 * 256)()) == code
+    assert lib.moe_last_error_string()
+
+
+ROPE = dict(q=P, q_st=4096, q_sh=64, q_out=P, qo_st=4096, qo_sh=64, kv=P, kv_st=576, gamma=P, eps=1e-6, kv_out=P,
+            kvo_st=576, cache=P, page_st=64 * 576, row_st=576, num_pages=4, page_size=64, slots=P, positions=P, freq=P,
+            amplitude=1.0, layout=0, T=4, H=64, dim=64, latent=512, dtype=0, stream=None)
+PAGED = dict(q=P, q_st=64 * 576, q_sh=576, Tq=4, cache=P, page_st=64 * 576, row_st=576, num_pages=9, page_size=64,
+             table=P, table_st=8, max_pages=8, ctx=P, cu_q=None, B=4, H=64, scale=0.07, dtype=0, out=P, o_st=64 * 512,
+             o_sh=512, lse=None, ws=P, ws_bytes=1 << 30, stream=None)
+RAGGED = dict(q=P, q_st=64 * 192, q_sh=192, Tq=4, kn=P, kn_st=64 * 256, kn_sh=256, kp=P, kp_st=64, v=P, v_st=64 * 256,
+              v_sh=256, Tk=4, cu_q=P, cu_k=P, B=1, max_q=4, H=64, scale=0.07, causal=1, dtype=0, out=P, o_st=64 * 128,
+              o_sh=128, lse=None, stream=None)
+PROJ = dict(x=P, x_st=64 * 128, x_sh=128, shared=0, w=P, w_sh=512 * 128, w_sr=128, w_kn=0, T=4, H=64, K=128, N=512,
+            dtype=0, out=P, o_st=64 * 512, o_sh=512, stream=None)
+ARG, UNS = _lib.MOE_ERR_ARG, _lib.MOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("call,base,change,code", [
+    ("mla_rope_append", ROPE, dict(dtype=2), ARG), ("mla_rope_append", ROPE, dict(dim=24), UNS),
+    ("mla_rope_append", ROPE, dict(dim=272), UNS), ("mla_rope_append", ROPE, dict(layout=2), ARG),
+    ("mla_rope_append", ROPE, dict(q=None, kv=None), ARG), ("mla_rope_append", ROPE, dict(q=ODD), ARG),
+    ("mla_rope_append", ROPE, dict(q_out=None), ARG), ("mla_rope_append", ROPE, dict(q_st=4097), ARG),
+    ("mla_rope_append", ROPE, dict(qo_sh=32), ARG), ("mla_rope_append", ROPE, dict(latent=4), UNS),
+    ("mla_rope_append", ROPE, dict(latent=2048), UNS), ("mla_rope_append", ROPE, dict(kv_out=None, cache=None), ARG),
+    ("mla_rope_append", ROPE, dict(row_st=512), ARG), ("mla_rope_append", ROPE, dict(slots=None), ARG),
+    ("mla_rope_append", ROPE, dict(page_size=0), UNS), ("mla_rope_append", ROPE, dict(eps=-1.0), ARG),
+    ("mla_rope_append", ROPE, dict(positions=None), ARG), ("mla_rope_append", ROPE, dict(freq=None), ARG),
+    ("mla_rope_append", ROPE, dict(T=-1), ARG), ("mla_rope_append", ROPE, dict(H=0), UNS),
+    ("mla_rope_append", ROPE, dict(amplitude=math.inf), ARG), ("mla_rope_append", ROPE, dict(kv_st=0), ARG),
+    ("mla_attn_paged", PAGED, dict(dtype=-1), ARG), ("mla_attn_paged", PAGED, dict(H=0), UNS),
+    ("mla_attn_paged", PAGED, dict(H=129), UNS), ("mla_attn_paged", PAGED, dict(scale=0.0), ARG),
+    ("mla_attn_paged", PAGED, dict(scale=math.nan), ARG), ("mla_attn_paged", PAGED, dict(B=-1), ARG),
+    ("mla_attn_paged", PAGED, dict(B=8193, Tq=8193), UNS), ("mla_attn_paged", PAGED, dict(Tq=5), ARG),
+    ("mla_attn_paged", PAGED, dict(page_size=12), UNS), ("mla_attn_paged", PAGED, dict(page_size=0), UNS),
+    ("mla_attn_paged", PAGED, dict(num_pages=0), UNS), ("mla_attn_paged", PAGED, dict(q=None), ARG),
+    ("mla_attn_paged", PAGED, dict(cache=ODD), ARG), ("mla_attn_paged", PAGED, dict(row_st=568), ARG),
+    ("mla_attn_paged", PAGED, dict(row_st=580), ARG), ("mla_attn_paged", PAGED, dict(table=None), ARG),
+    ("mla_attn_paged", PAGED, dict(table_st=7), ARG), ("mla_attn_paged", PAGED, dict(ctx=None), ARG),
+    ("mla_attn_paged", PAGED, dict(out=None), ARG), ("mla_attn_paged", PAGED, dict(o_sh=500), ARG),
+    ("mla_attn_paged", PAGED, dict(ws=None), ARG), ("mla_attn_paged", PAGED, dict(ws_bytes=1000), ARG),
+    ("mla_attn_paged", PAGED, dict(max_pages=-1), UNS), ("mla_attn_paged", PAGED, dict(q_sh=-8), ARG),
+    ("mla_attn_ragged", RAGGED, dict(dtype=3), ARG), ("mla_attn_ragged", RAGGED, dict(causal=2), ARG),
+    ("mla_attn_ragged", RAGGED, dict(H=0), UNS), ("mla_attn_ragged", RAGGED, dict(H=1025), UNS),
+    ("mla_attn_ragged", RAGGED, dict(B=65536), UNS), ("mla_attn_ragged", RAGGED, dict(Tk=-1), ARG),
+    ("mla_attn_ragged", RAGGED, dict(max_q=-1), ARG), ("mla_attn_ragged", RAGGED, dict(kn=None), ARG),
+    ("mla_attn_ragged", RAGGED, dict(v=ODD), ARG), ("mla_attn_ragged", RAGGED, dict(kp_st=60), ARG),
+    ("mla_attn_ragged", RAGGED, dict(cu_k=None), ARG), ("mla_attn_ragged", RAGGED, dict(o_st=64), ARG),
+    ("mla_attn_ragged", RAGGED, dict(scale=-1.0), ARG), ("mla_attn_ragged", RAGGED, dict(q_st=1 << 40), ARG),
+    ("mla_head_proj", PROJ, dict(dtype=9), ARG), ("mla_head_proj", PROJ, dict(shared=2), ARG),
+    ("mla_head_proj", PROJ, dict(w_kn=-1), ARG), ("mla_head_proj", PROJ, dict(K=12), UNS),
+    ("mla_head_proj", PROJ, dict(K=0), UNS), ("mla_head_proj", PROJ, dict(N=4), UNS),
+    ("mla_head_proj", PROJ, dict(N=16384), UNS), ("mla_head_proj", PROJ, dict(H=0), UNS),
+    ("mla_head_proj", PROJ, dict(T=-1), ARG), ("mla_head_proj", PROJ, dict(T=(1 << 20) + 1), UNS),
+    ("mla_head_proj", PROJ, dict(x=None), ARG), ("mla_head_proj", PROJ, dict(w=ODD), ARG),
+    ("mla_head_proj", PROJ, dict(w_sr=64), ARG), ("mla_head_proj", PROJ, dict(o_sh=256), ARG),
+    ("mla_head_proj", PROJ, dict(x_st=12), ARG),
+])
+def test_refusals(lib, call, base, change, code):
+    args = dict(base)
+    args.update(change)
+    assert getattr(lib, call)(*args.values()) == code
+    assert lib.moe_last_error_string() and lib.moe_last_launch_count() == 0
+
+
+def test_nothing_to_do(lib):
+    assert lib.mla_rope_append(*dict(ROPE, T=0, q=None, positions=None).values()) == _lib.MOE_OK
+    assert lib.mla_attn_paged(*dict(PAGED, B=0, Tq=0, q=None, ctx=None).values()) == _lib.MOE_OK
+    assert lib.mla_attn_ragged(*dict(RAGGED, Tq=0, q=None).values()) == _lib.MOE_OK
+    assert lib.mla_head_proj(*dict(PROJ, T=0, x=None).values()) == _lib.MOE_OK
+    assert lib.moe_last_launch_count() == 0
+    assert lib.mla_paged_workspace_bytes() > 0
+
+
+def test_binding_wants_cuda_tensors():
+    x = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        moe.mla_head_proj(x, torch.zeros(4, 8, 128, dtype=torch.bfloat16))
