@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 #include <utility>
 
@@ -75,6 +76,20 @@ cudaError_t launch_combine_residual_rmsnorm(const void *o, const float *w, const
 // entry points defined in other translation units. report_error returns code.
 int report_error(int code, const char *msg);
 void report_launches(int n);
+
+// Allows `kernel` the given dynamic shared memory, once per device (`done`: the devices
+// that have it, one flag word per kernel).
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // SMs of the current device; the driver's tensor-map encoder (NULL when it has none).
 int num_sms();

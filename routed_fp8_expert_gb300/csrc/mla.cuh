@@ -60,7 +60,11 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t tile
     return d;
 }
 
-// D[tmem] (+)= A[tmem] B[smem], kind::f16.
+// D[tmem] (+)= A[smem] B[smem] and D[tmem] (+)= A[tmem] B[smem], kind::f16.
+__device__ __forceinline__ void mma_16_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+    mma_bf16(d_tmem, a, b, idesc, accumulate);   // the element type is in the descriptor
+}
 __device__ __forceinline__ void mma_16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                           uint32_t accumulate) {
     asm volatile(
@@ -140,6 +144,33 @@ __device__ __forceinline__ void st_shared_v4(uint32_t dst, uint4 v) {
 
 __device__ __forceinline__ void st_shared_u32(uint32_t dst, uint32_t v) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+}
+
+// One lane of the (converged) warp. The compiler knows that a single lane runs what is
+// guarded by it: an MMA then issues in 27 cycles instead of the 48 it takes behind
+// `lane == 0` (64 x 64 x 16, measured), which decides whether small MMAs reach the
+// tensor rate.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// Whether the phase with the given parity has completed, without suspending.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // Bounded wait of a whole role: false once any role of the CTA has given up.

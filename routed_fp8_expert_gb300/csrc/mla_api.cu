@@ -209,6 +209,7 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
     if (B < 0) return fail(MOE_ERR_ARG, "B=%d is negative", B);
     MLA_CHECK(range(B, 0, 8192, "B"));
     MLA_CHECK(count(Tq, "Tq"));
+    MLA_CHECK(range(Tq * H, 0, (int64_t{1} << 31) - 1024, "Tq * H"));
     if (!cu_q && Tq != B)
         return fail(MOE_ERR_ARG, "Tq=%lld must equal B=%d when cu_q is NULL", static_cast<long long>(Tq), B);
     if (page_size <= 0 || page_size % 8 || page_size > (1 << 20))

@@ -90,16 +90,14 @@ __device__ __forceinline__ Seq read_seq(const PagedArgs &a, int b, bool report) 
     return s;
 }
 
-__device__ __forceinline__ int row_tiles(const Seq &s, int H) {
-    return static_cast<int>((static_cast<int64_t>(s.n) * H + kRows - 1) / kRows);
-}
+// (The rows of a call fit 31 bits: checked on the host.)
+__device__ __forceinline__ int row_tiles(const Seq &s, int H) { return (s.n * H + kRows - 1) / kRows; }
 
 // Keys that the last row of a row tile sees, and the key tiles that cover them (at
 // least one unit of work, so that rows without keys get their zeros).
 __device__ __forceinline__ int tile_keys(const Seq &s, int rt, int H) {
-    const int64_t last = min((static_cast<int64_t>(rt) + 1) * kRows, static_cast<int64_t>(s.n) * H) - 1;
-    const int64_t vis = static_cast<int64_t>(s.ctx) - s.n + last / H + 1;
-    return vis < 0 ? 0 : static_cast<int>(vis);
+    const int last = min((rt + 1) * kRows, s.n * H) - 1;
+    return max(0, s.ctx - s.n + last / H + 1);
 }
 __device__ __forceinline__ int units_of(int keys) { return keys <= kKeys ? 1 : (keys - 1) / kKeys + 1; }
 
@@ -330,57 +328,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kSoftWarps + 1) {
         // -------------------------------------------------------- MMA issue
-        if (lane == 0) {
+        // Two queues, each in order: the scores' column groups as they arrive, and the
+        // second products as their weights are ready, which go first because they free
+        // the ring. Neither waits for the other: a thread that blocked on a key tile
+        // would keep back the product whose end lets that tile be loaded.
+        if (elect_one()) {
             constexpr uint32_t id_s = idesc16(E::kFmt, kRows, kKeys);
             constexpr uint32_t id_o = idesc16(E::kFmt, 128, kRows, true, false);
+            const uint64_t dq = sdesc_sw128(sbase), dp = sdesc_sw128(sbase + kOffP);
+            const uint64_t dk = sdesc_sw128(sbase + kOffPairs), dr = sdesc_sw128(sbase + kOffRope);
+            const uint64_t dv = sdesc_mn_sw128(sbase + kOffPairs, kGroupBytes);
             Walk w;
             w.start(a, sh);
-            uint32_t s_tile = 0, p_tile = 0, seg = 0;
+            uint32_t s_tile = 0, p_tile = 0, seg = 0;   // tiles whose scores / products are next
             bool ok = true;
-            auto scores = [&](bool last) -> bool {
-                const uint32_t buf = s_tile & 1, ph = (s_tile >> 1) & 1;
-                if (!wait(smem_u32(&sh.s_empty[buf]), ph ^ 1, ERR_WAIT_PART_EMPTY)) return false;
-                const uint32_t d = tmem + kTmemS + buf * kKeys;
-                for (int g = 0; g <= kGroups; ++g) {
-                    const bool is_rope = g == kGroups;
-                    const int slot = is_rope ? buf : buf * kGroups + g;
-                    if (!wait(smem_u32(is_rope ? &sh.rope_full[slot] : &sh.pair_full[slot]), ph, ERR_WAIT_TMA_FULL)) return false;
-                    tc_fence_after();
-                    const uint32_t kb = sbase + (is_rope ? kOffRope + slot * kGroupBytes : kOffPairs + slot * kPairBytes);
-                    for (int c = 0; c < (is_rope ? 1 : 2); ++c)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(d, sdesc_sw128(sbase + (2 * g + c) * kRows * 128 + k * 32),
-                                     sdesc_sw128(kb + c * kGroupBytes + k * 32), id_s, g > 0 || c > 0 || k > 0);
-                }
-                mma_commit(smem_u32(&sh.s_full[buf]));
-                mma_commit(smem_u32(&sh.rope_empty[buf]));
-                if (last) mma_commit(smem_u32(&sh.q_empty));
-                ++s_tile;
-                return true;
-            };
             while (ok && w.next(a)) {
                 const int n = w.tiles();
                 if (n > 0) {
                     ok = wait(smem_u32(&sh.q_full), seg & 1, ERR_WAIT_TMA_FULL);
                     ++seg;
                     tc_fence_after();
-                    ok = ok && scores(n == 1);
-                    for (int j = 0; j < n && ok; ++j) {
-                        if (j + 1 < n && !scores(j + 2 == n)) { ok = false; break; }
-                        if (!wait(smem_u32(&sh.p_full), p_tile & 1, ERR_WAIT_PART_FULL)) { ok = false; break; }
-                        tc_fence_after();
-                        for (int g = 0; g < kGroups; ++g) {
-                            const int slot = (p_tile & 1) * kGroups + g;
-                            const uint32_t vb = sbase + kOffPairs + slot * kPairBytes;
+                    const uint32_t s_end = s_tile + n, p_first = p_tile, p_end = p_tile + n;
+                    int g = 0;   // next column group of s_tile
+                    unsigned idle = 0;
+                    unsigned long long t0 = 0;
+                    while (ok && p_tile != p_end) {
+                        if (s_tile != p_tile && mbar_test(smem_u32(&sh.p_full), p_tile & 1)) {
+                            tc_fence_after();
+                            const uint32_t half = p_tile & 1, acc0 = p_tile != p_first;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16(tmem + kTmemO + g * kRows, sdesc_mn_sw128(vb + k * 2048, kGroupBytes),
-                                         sdesc_sw128(sbase + kOffP + k * 32), id_o, j > 0 || k > 0);
-                            mma_commit(smem_u32(&sh.pair_empty[slot]));
+                            for (int m = 0; m < kGroups; ++m) {
+                                const uint64_t v = dv + ((half * kGroups + m) * kPairBytes >> 4);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_16_ss(tmem + kTmemO + m * kRows, v + (k * 2048 >> 4), dp + (k * 32 >> 4), id_o,
+                                              k > 0 ? 1 : acc0);
+                                mma_commit(smem_u32(&sh.pair_empty[half * kGroups + m]));
+                            }
+                            mma_commit(smem_u32(&sh.pv_done));
+                            ++p_tile;
+                            idle = 0;
+                            continue;
                         }
-                        mma_commit(smem_u32(&sh.pv_done));
-                        ++p_tile;
+                        if (s_tile != s_end) {
+                            const uint32_t buf = s_tile & 1, ph = (s_tile >> 1) & 1;
+                            const bool is_rope = g == kGroups;
+                            const int slot = is_rope ? buf : buf * kGroups + g;
+                            if ((g > 0 || mbar_test(smem_u32(&sh.s_empty[buf]), ph ^ 1)) &&
+                                mbar_test(smem_u32(is_rope ? &sh.rope_full[slot] : &sh.pair_full[slot]), ph)) {
+                                tc_fence_after();
+                                const uint32_t d = tmem + kTmemS + buf * kKeys;
+                                const uint64_t q = dq + (g * 2 * kRows * 128 >> 4);
+                                if (is_rope) {
+                                    const uint64_t k0 = dr + (slot * kGroupBytes >> 4);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) mma_16_ss(d, q + (k * 32 >> 4), k0 + (k * 32 >> 4), id_s, 1);
+                                    mma_commit(smem_u32(&sh.s_full[buf]));
+                                    mma_commit(smem_u32(&sh.rope_empty[buf]));
+                                    if (s_tile + 1 == s_end) mma_commit(smem_u32(&sh.q_empty));
+                                    ++s_tile;
+                                    g = 0;
+                                } else {
+                                    const uint64_t k0 = dk + (slot * kPairBytes >> 4);
+                                    const uint32_t acc0 = g > 0;
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k)
+                                        mma_16_ss(d, q + ((k >> 2) * kRows * 128 + (k & 3) * 32 >> 4),
+                                                  k0 + ((k >> 2) * kGroupBytes + (k & 3) * 32 >> 4), id_s, k > 0 ? 1 : acc0);
+                                    ++g;
+                                }
+                                idle = 0;
+                                continue;
+                            }
+                        }
+                        // bounded: after the limit, or when another role gave up, leave
+                        if ((++idle & 1023u) == 0) {
+                            const unsigned long long t = globaltimer();
+                            if (idle == 1024u) t0 = t;
+                            if (ld_volatile_shared(wait.abort_addr)) ok = false;
+                            else if (t - t0 > kWaitLimitNs) {
+                                st_volatile_shared(wait.abort_addr, 1);
+                                record_error(a.err, ERR_WAIT_TMA_FULL);
+                                ok = false;
+                            }
+                        }
                     }
                 }
                 w.advance();
@@ -399,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Walk w;
         w.start(a, sh);
         uint32_t tile = 0, seg = 0;
-        int4 join = make_int4(-1, 0, 0, 0);
+        int4 join = make_int4(0, 0, 0, 0);
         // after a wait that gave up a thread waits no more but keeps to the loops, so
         // that every named barrier still gets all of its threads
         bool ok = true;
@@ -408,28 +439,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         while (w.next(a)) {
             const int n = w.tiles();
-            const int64_t r0 = static_cast<int64_t>(w.rt) * kRows;
-            const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(w.s.n) * a.H - r0));
+            const int r0 = w.rt * kRows;
+            const int rows = min(kRows, w.s.n * a.H - r0);
             const bool whole = w.k0 == 0 && w.k1 == w.kt;
             auto visible = [&](int r) {
-                if (r >= rows) return 0;
-                const int64_t v = static_cast<int64_t>(w.s.ctx) - w.s.n + (r0 + r) / a.H + 1;
-                return v < 0 ? 0 : static_cast<int>(v);
+                return r >= rows ? 0 : max(0, w.s.ctx - w.s.n + (r0 + r) / a.H + 1);
             };
             const int vis_a = visible(ra), vis_b = visible(rb);
             float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
             if (n > 0) {
                 // Q into shared memory (128-byte swizzle); rows past the sequence are zero
                 if (seg > 0) hold(&sh.q_empty, (seg - 1) & 1, ERR_WAIT_PART_EMPTY);
-                for (int i = tid; i < kRows * (kMlaWidth / 8); i += kSoftThreads) {
-                    const int r = i / (kMlaWidth / 8), v = i - r * (kMlaWidth / 8);
-                    const uint32_t dst = sbase + (v >> 3) * kRows * 128 + r * 128 + (((v & 7) ^ (r & 7)) << 4);
-                    if (r < rows) {
-                        const int64_t row = r0 + r, t = row / a.H, h = row - t * a.H;
-                        cp_async_16(dst, static_cast<const T *>(a.q) + (w.s.row0 + t) * a.q_st + h * a.q_sh + v * 8);
-                    } else {
-                        st_shared_v4(dst, make_uint4(0, 0, 0, 0));
+                {
+                    // eight threads take a row's 72 vectors, 16 rows at a time
+                    const T *src[kRows / 16];
+#pragma unroll
+                    for (int i = 0; i < kRows / 16; ++i) {
+                        const int r = tid / 8 + 16 * i, t = (r0 + r) / a.H, h = r0 + r - t * a.H;
+                        src[i] = r < rows ? static_cast<const T *>(a.q) + (w.s.row0 + t) * a.q_st + h * a.q_sh : nullptr;
                     }
+#pragma unroll
+                    for (int c = 0; c < kMlaWidth / 64; ++c)
+#pragma unroll
+                        for (int i = 0; i < kRows / 16; ++i) {
+                            const int r = tid / 8 + 16 * i, v = tid & 7;
+                            const uint32_t dst = sbase + c * kRows * 128 + r * 128 + ((v ^ (r & 7)) << 4);
+                            if (src[i]) cp_async_16(dst, src[i] + c * 64 + v * 8);
+                            else st_shared_v4(dst, make_uint4(0, 0, 0, 0));
+                        }
                 }
                 cp_async_wait_all();
                 fence_async_smem();
@@ -534,12 +571,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 2; ++e) {
                     const int r = e ? rb : ra;
                     const float l = e ? l_b : l_a, m = e ? m_b : m_a;
-                    const int64_t row = r0 + r, t = row / a.H, h = row - t * a.H;
+                    const int t = (r0 + r) / a.H, h = r0 + r - t * a.H;
                     if (whole) {
                         sh.factor[r] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
                         sh.row_off[r] = r < rows ? (w.s.row0 + t) * a.o_st + h * a.o_sh : -1;
                         if (a.lse && r < rows)
-                            a.lse[(w.s.row0 + t) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                            a.lse[static_cast<int64_t>(w.s.row0 + t) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                     } else if (r < rows) {
                         a.part_ml[static_cast<int64_t>(slot) * kRows + r] = make_float2(m, l);
                     }
@@ -581,8 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t last = w.at + (w.kt - 1);
                 int64_t c_end = blockIdx.x;
                 while (part_lo(sh.total, sh.parts, static_cast<int>(c_end) + 1) <= last) ++c_end;
-                join = make_int4(w.s.row0, static_cast<int>(r0), rows, static_cast<int>(c_end));
-                join.x = w.b;
+                join = make_int4(w.s.row0, r0, rows, static_cast<int>(c_end));
             }
             w.advance();
         }
@@ -594,82 +630,123 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partial results of the items that several CTAs shared: row by row
 //   M = max m_s,  O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s
-// over the item's parts in order. joins[c] = (sequence, first row, rows, last CTA) of
-// the item whose first part CTA c holds (sequence -1: none). Four groups of 128
+// over the item's parts in order. joins[c] = (the sequence's first query, first row of
+// the tile, rows, last CTA) of the item whose first part CTA c holds (rows 0: none). Four groups of 128
 // threads take every fourth part of a row, four columns each.
 constexpr int kJoinThreads = 512;
+constexpr int kMaxCtas = 256;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs a, int ctas) {
-    __shared__ int4 s_join[256];
-    __shared__ float s_w[256];
+    __shared__ int s_rows[kMaxCtas + 1];   // rows of the joins before join c
+    __shared__ int s_sum[kMaxCtas / 32];
+    __shared__ float s_w[kMaxCtas];
+    __shared__ float s_l;
     __shared__ float4 s_acc[3][128];
     pdl_trigger();
     pdl_wait();
-    const int tid = threadIdx.x;
-    for (int i = tid; i < ctas; i += kJoinThreads) s_join[i] = a.joins[i];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int4 mine = tid < ctas ? a.joins[tid] : make_int4(0, 0, 0, 0);
+    int inc = mine.z;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31 && warp < kMaxCtas / 32) s_sum[warp] = inc;
     __syncthreads();
-    int first = 0;   // rows of the joins before join c
-    for (int c = 0; c < ctas; ++c) {
-        const int4 j = s_join[c];
-        if (j.x < 0) continue;
-        // rows of this join that fall to this block
-        int r = (static_cast<int>(blockIdx.x) - first) % static_cast<int>(gridDim.x);
-        if (r < 0) r += gridDim.x;
-        first += j.z;
-        for (; r < j.z; r += gridDim.x) {
-            const int parts = j.w - c + 1;
-            auto slot_of = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * kRows + r; };
-            float M = -INFINITY, L = 0.f;
-            __syncthreads();
-            if (tid < 32) {
-                for (int s = tid; s < parts; s += 32) M = fmaxf(M, a.part_ml[slot_of(s)].x);
+    if (tid < kMaxCtas) {
+        for (int i = 0; i < warp; ++i) inc += s_sum[i];
+        s_rows[tid + 1] = inc;
+        if (tid == 0) s_rows[0] = 0;
+    }
+    __syncthreads();
+    const int total = s_rows[kMaxCtas];
+    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+        int lo = 0, hi = kMaxCtas;   // the join with s_rows[lo] <= i < s_rows[lo + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            (s_rows[mid] <= i ? lo : hi) = mid;
+        }
+        const int c = lo, r = i - s_rows[c];
+        const int4 j = a.joins[c];
+        const int parts = j.w - c + 1;
+        auto slot_of = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * kRows + r; };
+        const int grp = tid >> 7, col = tid & 127;
+        // the first sums are on their way while the weights are formed
+        constexpr int kAhead = 8;
+        float4 v[kAhead];
 #pragma unroll
-                for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                for (int s = tid; s < parts; s += 32) {
-                    const float2 ml = a.part_ml[slot_of(s)];
-                    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-                    s_w[s] = w;
-                    L += w * ml.y;
-                }
+        for (int k = 0; k < kAhead; ++k) {
+            const int s = grp + 4 * k;
+            v[k] = s < parts ? *reinterpret_cast<const float4 *>(a.part_o + slot_of(s) * kMlaLatent + col * 4)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float M = -INFINITY;
+        if (warp == 0) {
+            float2 ml[kMaxCtas / 32];
+            float L = 0.f;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-                __syncwarp();
-                const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);
-                for (int s = tid; s < parts; s += 32) s_w[s] *= inv;
+            for (int k = 0; k < kMaxCtas / 32; ++k) {
+                const int s = lane + 32 * k;
+                ml[k] = s < parts ? a.part_ml[slot_of(s)] : make_float2(-INFINITY, 0.f);
+                M = fmaxf(M, ml[k].x);
             }
-            __syncthreads();
-            const int grp = tid >> 7, col = tid & 127;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int s = grp; s < parts; s += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(a.part_o + slot_of(s) * kMlaLatent + col * 4);
-                const float w = s_w[s];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+            for (int k = 0; k < kMaxCtas / 32; ++k) {
+                ml[k].x = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
+                L += ml[k].x * ml[k].y;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);
+#pragma unroll
+            for (int k = 0; k < kMaxCtas / 32; ++k)
+                if (lane + 32 * k < parts) s_w[lane + 32 * k] = ml[k].x * inv;
+            if (lane == 0) s_l = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        }
+        __syncthreads();
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = grp; s0 < parts; s0 += 4 * kAhead) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int s = s0 + 4 * k;
                 // a part without visible keys has weight zero and sums of zero
-                acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
-            }
-            if (grp > 0) s_acc[grp - 1][col] = acc;
-            __syncthreads();
-            if (grp == 0) {
-#pragma unroll
-                for (int g = 0; g < 3; ++g) {
-                    const float4 v = s_acc[g][col];
-                    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+                if (s < parts) {
+                    const float w = s_w[s];
+                    acc.x += w * v[k].x, acc.y += w * v[k].y, acc.z += w * v[k].z, acc.w += w * v[k].w;
                 }
-                const Seq sq = read_seq(a, j.x, false);
-                const int64_t row = static_cast<int64_t>(j.y) + r, t = row / a.H, h = row - t * a.H;
-                T *dst = static_cast<T *>(a.out) + (sq.row0 + t) * a.o_st + h * a.o_sh + col * 4;
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(Elem<T>::pack(acc.x, acc.y), Elem<T>::pack(acc.z, acc.w));
-                if (a.lse && tid == 0)
-                    a.lse[(sq.row0 + t) * a.H + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int s = s0 + 4 * (kAhead + k);
+                if (s < parts) v[k] = *reinterpret_cast<const float4 *>(a.part_o + slot_of(s) * kMlaLatent + col * 4);
             }
         }
+        if (grp > 0) s_acc[grp - 1][col] = acc;
+        __syncthreads();
+        if (grp == 0) {
+#pragma unroll
+            for (int g = 0; g < 3; ++g) {
+                const float4 x = s_acc[g][col];
+                acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+            }
+            const int t = (j.y + r) / a.H, h = j.y + r - t * a.H;
+            const int64_t q = j.x + t;
+            T *dst = static_cast<T *>(a.out) + q * a.o_st + h * a.o_sh + col * 4;
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(Elem<T>::pack(acc.x, acc.y), Elem<T>::pack(acc.z, acc.w));
+            if (a.lse && tid == 0) a.lse[q * a.H + h] = s_l;
+        }
+        __syncthreads();   // s_w, s_l and s_acc are reused by the next row
     }
 }
 
 template <typename T>
 cudaError_t launch_t(const CUtensorMap &lat, const CUtensorMap &rope, const PagedArgs &a, int grid, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(paged_attn_kernel<T>, kSmem, done);
     if (e != cudaSuccess) return e;
     e = launch_pdl(paged_attn_kernel<T>, dim3(grid), dim3(kThreads), kSmem, stream, lat, rope, a);
     if (e != cudaSuccess) return e;
@@ -680,7 +757,7 @@ cudaError_t launch_t(const CUtensorMap &lat, const CUtensorMap &rope, const Page
 
 cudaError_t launch_paged(const CUtensorMap &latent, const CUtensorMap &rope, const PagedArgs &a, bool bf16, int grid,
                          cudaStream_t stream) {
-    if (grid > 256) return cudaErrorInvalidValue;   // the join keeps one entry per CTA in shared memory
+    if (grid > kMaxCtas) return cudaErrorInvalidValue;
     return bf16 ? launch_t<__nv_bfloat16>(latent, rope, a, grid, stream)
                 : launch_t<__half>(latent, rope, a, grid, stream);
 }

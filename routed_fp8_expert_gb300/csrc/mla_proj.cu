@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 5) {
         // -------------------------------------------------------- MMA issue
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id = idesc16(E::kFmt, kTile, kTile, false, KN);
             uint32_t it = 0, n = 0;
             bool ok = true;
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t xa = sbase + st * kStageBytes, wb = xa + kABytes;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + buf * kTile, sdesc_sw128(xa + k * 32),
+                        mma_16_ss(tmem + buf * kTile, sdesc_sw128(xa + k * 32),
                                  KN ? sdesc_mn_sw128(wb + k * 2048, kBBytes / 2) : sdesc_sw128(wb + k * 32), id,
                                  c > 0 || k > 0);
                     mma_commit(smem_u32(&sh.empty[st]));
@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <typename T, bool KN>
 cudaError_t launch_t(const CUtensorMap &x, const CUtensorMap &w, const ProjArgs &a, int num_sms, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(head_proj_kernel<T, KN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(head_proj_kernel<T, KN>, kSmem, done);
     if (e != cudaSuccess) return e;
     const int64_t total = static_cast<int64_t>((a.T + kTile - 1) / kTile) * a.H * ((a.N + kTile - 1) / kTile);
     const int grid = total < num_sms ? static_cast<int>(total) : num_sms;

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 9) {
         // -------------------------------------------------------- MMA issue
-        if (lane == 0 && tiles > 0) {
+        if (tiles > 0 && elect_one()) {
             constexpr uint32_t id_s = idesc16(E::kFmt, kTile, kTile);
             constexpr uint32_t id_o = idesc16(E::kFmt, kTile, kMlaV, false, true);
             constexpr uint32_t id_o64 = idesc16(E::kFmt, kTile, 64, false, true);
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t kb = sbase + kOffRing + slot_of(piece) * kPiece;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + t * kTile, sdesc_sw128(sbase + (t * kQPieces + c) * kPiece + k * 32),
+                        mma_16_ss(tmem + t * kTile, sdesc_sw128(sbase + (t * kQPieces + c) * kPiece + k * 32),
                                  sdesc_sw128(kb + k * 32), id_s, c > 0 || k > 0);
                     if (t == nt - 1) mma_commit(smem_u32(&sh.empty[slot_of(piece)]));
                 }
@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T>
 cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &kn, const CUtensorMap &kp, const CUtensorMap &v,
                      const RaggedArgs &a, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(ragged_attn_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(ragged_attn_kernel<T>, kSmem, done);
     if (e != cudaSuccess) return e;
     return launch_pdl(ragged_attn_kernel<T>, dim3((a.max_q + kQRows - 1) / kQRows, a.H, a.B), dim3(kThreads), kSmem,
                       stream, q, kn, kp, v, a);

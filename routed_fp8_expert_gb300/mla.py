@@ -13,59 +13,75 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import MOE_ERR_ARG, RMS_NORM_EPS, MoeError, _check, _cuda, _p, _stream, load
+from ._lib import MOE_ERR_ARG, RMS_NORM_EPS, MoeError, _check, _p, load
 
 MLA_LATENT, MLA_ROPE, MLA_NOPE, MLA_V = 512, 64, 128, 128
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 _LAYOUTS = {"interleaved": 0, "half": 1}
 
 
+# the raw handle: building a torch.cuda.Stream object costs more than a small launch
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _bad(msg):
     raise MoeError(MOE_ERR_ARG, msg)
 
 
-def _dtype(*named):
-    """The dtype code shared by the given (name, tensor) pairs."""
-    first = named[0][1].dtype
-    if first not in _DTYPES:
-        _bad(f"{named[0][0]} must be bf16 or fp16, not {first}")
-    for name, t in named:
-        if t.dtype != first:
-            _bad(f"{name} is {t.dtype}, {named[0][0]} is {first}")
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            _bad(f"the innermost dimension of {name} must be contiguous")
-    return _DTYPES[first]
+def _index(t):
+    """CUDA device index of the tensor that names a call's device."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    return i
 
 
-def _device(*ts):
-    """All tensors on one CUDA device."""
-    _cuda(*ts)
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) > 1:
-        _bad(f"tensors on several devices: {sorted(map(str, devs))}")
+def _ok(name, t, shape, dtype, index):
+    """Refuse a tensor of another shape, type, device or a strided innermost dimension."""
+    if t.shape == shape and t.dtype == dtype and t.get_device() == index and (shape[-1] < 2 or t.stride(-1) == 1):
+        return
+    if t.get_device() < 0:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.shape != shape:
+        _bad(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        _bad(f"{name} is {t.dtype}, expected {dtype}")
+    if t.get_device() != index:
+        _bad(f"{name} is on device {t.get_device()}, the call on {index}")
+    _bad(f"the innermost dimension of {name} must be contiguous")
 
 
-def _shape(name, t, *want):
-    if t.dim() != len(want) or any(w is not None and s != w for s, w in zip(t.shape, want)):
-        _bad(f"{name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in want)}")
+def _code(name, t):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        _bad(f"{name} must be bf16 or fp16, not {t.dtype}")
+    return code
 
 
-def _int32(name, t, *want):
-    _shape(name, t, *want)
-    if t.dtype != torch.int32:
-        _bad(f"{name} must be int32, not {t.dtype}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        _bad(f"the innermost dimension of {name} must be contiguous")
+def _dims(name, t, n):
+    if t.dim() != n:
+        _bad(f"{name} has shape {tuple(t.shape)}, expected {n} dimensions")
+    return t.shape
 
 
-def _st(t, dim, width=0):
-    """Stride of a dimension; a dimension of one has any stride, so it gets a legal one."""
-    return t.stride(dim) if t.shape[dim] > 1 else max(8, (width + 7) // 8 * 8)
+def _pad8(n):
+    return max(8, (n + 7) & ~7)
 
 
-def _th(t):
-    """Token and head strides of [T, H, width]."""
-    return _st(t, 0, t.shape[1] * t.shape[2] if t.shape[1] == 1 else max(t.shape[2], t.stride(1))), _st(t, 1, t.shape[2])
+def _row(t):
+    """Row stride of a matrix; a dimension of one may carry any stride, so it gets a legal one."""
+    return t.stride(0) if t.shape[0] > 1 else _pad8(t.shape[1])
+
+
+def _pair(t):
+    """The two outer strides of a 3D tensor, legal for dimensions of one."""
+    s0, s1, _ = t.stride()
+    n0, n1, w = t.shape
+    if n1 <= 1:
+        s1 = _pad8(w)
+    if n0 <= 1:
+        s0 = _pad8(max(w, s1))
+    return s0, s1
 
 
 @dataclass
@@ -105,48 +121,59 @@ def mla_rope_append(q_pe, kv, positions, plan: RopePlan, gamma=None, eps: float 
     ref = q_pe if q_pe is not None else kv
     if ref is None:
         _bad("q_pe and kv are both None")
-    _device(q_pe, kv, positions, plan.freq, gamma, cache, slots, q_out, kv_out)
-    T, dim = ref.shape[0], plan.dim
-    H, latent = 1, 0
+    dev, ty, dim, T = _index(ref), ref.dtype, plan.dim, ref.shape[0]
+    code = _code("q_pe" if q_pe is not None else "kv", ref)
+    H = 1
+    latent = pages = pq = pqo = pkv = pg = pko = pc = psl = q_st = q_sh = qo_st = qo_sh = 0
+    kv_st = ko_st = c_st = c_sr = 0
+    page = 1
     if q_pe is not None:
-        _shape("q_pe", q_pe, T, None, dim)
-        H = q_pe.shape[1]
-        q_out = torch.empty((T, H, dim), dtype=q_pe.dtype, device=q_pe.device) if q_out is None else q_out
-        _shape("q_out", q_out, T, H, dim)
+        H = _dims("q_pe", q_pe, 3)[1]
+        _ok("q_pe", q_pe, (T, H, dim), ty, dev)
+        if q_out is None:
+            q_out = torch.empty((T, H, dim), dtype=ty, device=ref.device)
+        else:
+            _ok("q_out", q_out, (T, H, dim), ty, dev)
+        q_st, q_sh = _pair(q_pe)
+        qo_st, qo_sh = _pair(q_out)
+        pq, pqo = q_pe.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         _bad("q_out is given without q_pe")
     if kv is not None:
-        _shape("kv", kv, T, None)
-        latent = kv.shape[1] - dim
-        if cache is None and kv_out is None:
-            kv_out = torch.empty((T, latent + dim), dtype=kv.dtype, device=kv.device)
+        width = _dims("kv", kv, 2)[1]
+        latent = width - dim
+        _ok("kv", kv, (T, width), ty, dev)
+        pkv, kv_st = kv.data_ptr(), _row(kv)
         if kv_out is not None:
-            _shape("kv_out", kv_out, T, latent + dim)
+            _ok("kv_out", kv_out, (T, width), ty, dev)
+        elif cache is None:
+            kv_out = torch.empty((T, width), dtype=ty, device=ref.device)
+        if kv_out is not None:
+            pko, ko_st = kv_out.data_ptr(), _row(kv_out)
         if gamma is not None:
-            _shape("gamma", gamma, latent)
+            _ok("gamma", gamma, (latent,), ty, dev)
+            pg = gamma.data_ptr()
         if cache is not None:
-            _shape("cache", cache, None, None, latent + dim)
             if slots is None:
                 _bad("cache is given without slots")
-            _int32("slots", slots, T)
+            pages, page, _ = _dims("cache", cache, 3)
+            _ok("cache", cache, (pages, page, width), ty, dev)
+            _ok("slots", slots, (T,), torch.int32, dev)
+            c_st, c_sr = _pair(cache)
+            pc, psl = cache.data_ptr(), slots.data_ptr()
     elif cache is not None or kv_out is not None:
         _bad("cache or kv_out is given without kv")
-    _int32("positions", positions, T)
-    dt = _dtype(*[(n, t) for n, t in (("q_pe", q_pe), ("kv", kv), ("q_out", q_out), ("kv_out", kv_out),
-                                      ("gamma", gamma), ("cache", cache)) if t is not None])
-    q_s, qo_s = (_th(q_pe), _th(q_out)) if q_pe is not None else ((0, 0), (0, 0))
-    w = latent + dim
-    _check(load().mla_rope_append(
-        _p(q_pe), *q_s, _p(q_out), *qo_s, _p(kv), _st(kv, 0, w) if kv is not None else 0, _p(gamma), float(eps),
-        _p(kv_out), _st(kv_out, 0, w) if kv_out is not None else 0,
-        _p(cache), _st(cache, 0, w) if cache is not None else 0, _st(cache, 1, w) if cache is not None else 0,
-        cache.shape[0] if cache is not None else 0, cache.shape[1] if cache is not None else 1, _p(slots),
-        _p(positions), _p(plan.freq), plan.amplitude, plan.layout, T, H, dim, latent, dt, _stream(ref.device)))
+    _ok("positions", positions, (T,), torch.int32, dev)
+    _ok("plan.freq", plan.freq, (dim // 2,), torch.int64, dev)
+    _check(load().mla_rope_append(pq, q_st, q_sh, pqo, qo_st, qo_sh, pkv, kv_st, pg, eps, pko, ko_st, pc, c_st, c_sr,
+                                  pages, page, psl, positions.data_ptr(), plan.freq.data_ptr(), plan.amplitude,
+                                  plan.layout, T, H, dim, latent, code, _raw_stream(dev)))
     return q_out, kv_out
 
 
 def mla_paged_workspace(device=None) -> torch.Tensor:
-    """Workspace of mla_attn_paged: one size for every call on the device."""
+    """Workspace of mla_attn_paged: one size for every call on the device. Calls that
+    may overlap (on several streams) need one each."""
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
         n = load().mla_paged_workspace_bytes()
         return torch.empty(n, dtype=torch.uint8, device="cuda")
@@ -158,26 +185,31 @@ def mla_attn_paged(q, cache, block_table, ctx_lens, scale: float, cu_q=None, out
     block_table [B, max_pages], ctx_lens [B] (tokens in the cache, the new ones included)
     and cu_q [B + 1] are int32; cu_q None: one query per sequence. Causal: each query sees
     the keys up to its own. Returns out [Tq, H, 512] (and lse [Tq, H] fp32)."""
-    _device(q, cache, block_table, ctx_lens, cu_q, out, ws)
-    _shape("q", q, None, None, MLA_LATENT + MLA_ROPE)
-    _shape("cache", cache, None, None, MLA_LATENT + MLA_ROPE)
-    _int32("block_table", block_table, None, None)
-    B, max_pages = block_table.shape
-    _int32("ctx_lens", ctx_lens, B)
+    dev, ty = _index(q), q.dtype
+    code, width = _code("q", q), MLA_LATENT + MLA_ROPE
+    Tq, H, _ = _dims("q", q, 3)
+    pages, page, _ = _dims("cache", cache, 3)
+    B, max_pages = _dims("block_table", block_table, 2)
+    _ok("q", q, (Tq, H, width), ty, dev)
+    _ok("cache", cache, (pages, page, width), ty, dev)
+    _ok("block_table", block_table, (B, max_pages), torch.int32, dev)
+    _ok("ctx_lens", ctx_lens, (B,), torch.int32, dev)
     if cu_q is not None:
-        _int32("cu_q", cu_q, B + 1)
-    Tq, H = q.shape[0], q.shape[1]
-    dev = q.device
-    out = torch.empty((Tq, H, MLA_LATENT), dtype=q.dtype, device=dev) if out is None else out
-    _shape("out", out, Tq, H, MLA_LATENT)
-    dt = _dtype(("q", q), ("cache", cache), ("out", out))
-    lse = torch.empty((Tq, H), dtype=torch.float32, device=dev) if want_lse else None
-    ws = mla_paged_workspace(dev) if ws is None else ws
-    w = MLA_LATENT + MLA_ROPE
+        _ok("cu_q", cu_q, (B + 1,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((Tq, H, MLA_LATENT), dtype=ty, device=q.device)
+    else:
+        _ok("out", out, (Tq, H, MLA_LATENT), ty, dev)
+    lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device) if want_lse else None
+    if ws is None:
+        ws = mla_paged_workspace(q.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        _bad("ws must be contiguous and on the call's device")
     _check(load().mla_attn_paged(
-        _p(q), *_th(q), Tq, _p(cache), _st(cache, 0, w), _st(cache, 1, w), cache.shape[0], cache.shape[1],
-        _p(block_table), block_table.stride(0) if B > 1 else max_pages, max_pages, _p(ctx_lens), _p(cu_q), B, H,
-        float(scale), dt, _p(out), *_th(out), _p(lse), _p(ws), ws.numel() * ws.element_size(), _stream(dev)))
+        q.data_ptr(), *_pair(q), Tq, cache.data_ptr(), *_pair(cache), pages, page, block_table.data_ptr(),
+        block_table.stride(0) if B > 1 else max_pages, max_pages, ctx_lens.data_ptr(),
+        None if cu_q is None else cu_q.data_ptr(), B, H, scale, code, out.data_ptr(), *_pair(out),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(dev)))
     return (out, lse) if want_lse else out
 
 
@@ -187,47 +219,46 @@ def mla_attn_ragged(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, scale: float, ca
     (views of one tensor, if so), k_pe [Tk, 64] shared by the heads, cu_q and cu_k
     [B + 1] int32 row offsets, max_q at least the longest query run. Causal masks align
     the last query with the last key. Returns out [Tq, H, 128] (and lse [Tq, H] fp32)."""
-    _device(q, k_nope, k_pe, v, cu_q, cu_k, out)
-    _shape("q", q, None, None, MLA_NOPE + MLA_ROPE)
-    Tq, H = q.shape[0], q.shape[1]
-    _shape("k_nope", k_nope, None, H, MLA_NOPE)
-    Tk = k_nope.shape[0]
-    _shape("k_pe", k_pe, Tk, MLA_ROPE)
-    _shape("v", v, Tk, H, MLA_V)
-    _int32("cu_q", cu_q, None)
-    _int32("cu_k", cu_k, cu_q.shape[0])
-    B = cu_q.shape[0] - 1
+    dev, ty, code = _index(q), q.dtype, _code("q", q)
+    Tq, H, _ = _dims("q", q, 3)
+    Tk = _dims("k_nope", k_nope, 3)[0]
+    B = _dims("cu_q", cu_q, 1)[0] - 1
     if B < 0:
         _bad("cu_q is empty")
-    dev = q.device
-    out = torch.empty((Tq, H, MLA_V), dtype=q.dtype, device=dev) if out is None else out
-    _shape("out", out, Tq, H, MLA_V)
-    dt = _dtype(("q", q), ("k_nope", k_nope), ("k_pe", k_pe), ("v", v), ("out", out))
-    lse = torch.empty((Tq, H), dtype=torch.float32, device=dev) if want_lse else None
+    _ok("q", q, (Tq, H, MLA_NOPE + MLA_ROPE), ty, dev)
+    _ok("k_nope", k_nope, (Tk, H, MLA_NOPE), ty, dev)
+    _ok("k_pe", k_pe, (Tk, MLA_ROPE), ty, dev)
+    _ok("v", v, (Tk, H, MLA_V), ty, dev)
+    _ok("cu_q", cu_q, (B + 1,), torch.int32, dev)
+    _ok("cu_k", cu_k, (B + 1,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((Tq, H, MLA_V), dtype=ty, device=q.device)
+    else:
+        _ok("out", out, (Tq, H, MLA_V), ty, dev)
+    lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device) if want_lse else None
     _check(load().mla_attn_ragged(
-        _p(q), *_th(q), Tq, _p(k_nope), *_th(k_nope), _p(k_pe), _st(k_pe, 0, MLA_ROPE), _p(v), *_th(v), Tk, _p(cu_q),
-        _p(cu_k), B, int(max_q), H, float(scale), int(causal), dt, _p(out), *_th(out), _p(lse), _stream(dev)))
+        q.data_ptr(), *_pair(q), Tq, k_nope.data_ptr(), *_pair(k_nope), k_pe.data_ptr(), _row(k_pe), v.data_ptr(),
+        *_pair(v), Tk, cu_q.data_ptr(), cu_k.data_ptr(), B, max_q, H, scale, 1 if causal else 0, code, out.data_ptr(),
+        *_pair(out), None if lse is None else lse.data_ptr(), _raw_stream(dev)))
     return (out, lse) if want_lse else out
 
 
 def mla_head_proj(x, w, w_kn: bool = False, out=None):
     """out[t, h] = x[t, h] W_h with x [T, H, K] (or [T, 1, K], the same for every head) and
     w [H, N, K], or [H, K, N] with w_kn. Returns out [T, H, N]."""
-    _device(x, w, out)
-    _shape("w", w, None, None, None)
-    H = w.shape[0]
-    K, N = (w.shape[1], w.shape[2]) if w_kn else (w.shape[2], w.shape[1])
-    _shape("x", x, None, None, K)
-    shared = x.shape[1] == 1
-    if not shared and x.shape[1] != H:
-        _bad(f"x has {x.shape[1]} heads, w has {H}")
-    T = x.shape[0]
-    out = torch.empty((T, H, N), dtype=x.dtype, device=x.device) if out is None else out
-    _shape("out", out, T, H, N)
-    dt = _dtype(("x", x), ("w", w), ("out", out))
-    x_st, x_sh = _th(x)
-    o_st, o_sh = _th(out)
-    _check(load().mla_head_proj(_p(x), x_st, x_sh, int(shared), _p(w), _st(w, 0, w.shape[1] * w.shape[2]),
-                                _st(w, 1, w.shape[2]), int(w_kn), T, H, K, N, dt, _p(out), o_st, o_sh,
-                                _stream(x.device)))
+    dev, ty, code = _index(x), x.dtype, _code("x", x)
+    H, N, K = _dims("w", w, 3)
+    if w_kn:
+        N, K = K, N
+    T, xh, _ = _dims("x", x, 3)
+    if xh != 1 and xh != H:
+        _bad(f"x has {xh} heads, w has {H}")
+    _ok("x", x, (T, xh, K), ty, dev)
+    _ok("w", w, (H, K, N) if w_kn else (H, N, K), ty, dev)
+    if out is None:
+        out = torch.empty((T, H, N), dtype=ty, device=x.device)
+    else:
+        _ok("out", out, (T, H, N), ty, dev)
+    _check(load().mla_head_proj(x.data_ptr(), *_pair(x), 1 if xh == 1 else 0, w.data_ptr(), *_pair(w),
+                                1 if w_kn else 0, T, H, K, N, code, out.data_ptr(), *_pair(out), _raw_stream(dev)))
     return out
