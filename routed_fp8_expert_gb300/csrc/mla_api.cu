@@ -260,7 +260,7 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
     CUtensorMap lat, rope;
     const int64_t dims[4] = {64, page_size, kMlaWidth / 64, num_pages};
     const int64_t strides[3] = {row_st, 64, page_st};
-    const int box2[4] = {64, a.box_rows, a.box_rows == 64 ? 2 : 1, 1};
+    const int box2[4] = {64, a.box_rows, 2, 1};
     const int box1[4] = {64, a.box_rows, 1, 1};
     MLA_CHECK(tensor_map(&lat, cache, dtype, 4, dims, strides, box2, "latents"));
     MLA_CHECK(tensor_map(&rope, cache, dtype, 4, dims, strides, box1, "rotary keys"));

@@ -35,6 +35,7 @@ constexpr int kPairBytes = 2 * kKeys * 128;      // 16 KB
 constexpr int kGroupBytes = kKeys * 128;         // 8 KB
 constexpr int kPairSlots = 2 * kGroups;
 constexpr int kRopeSlots = 2;
+constexpr int kMaxSubs = 8;                      // boxes per key tile: pages of 8 rows
 constexpr int kQBytes = (kMlaWidth / 64) * kRows * 128;
 constexpr int kOffP = kQBytes;
 constexpr int kOffPairs = kOffP + kRows * 128;
@@ -43,7 +44,7 @@ constexpr int kOffMisc = kOffRope + kRopeSlots * kGroupBytes;
 constexpr int kSmem = kOffMisc + 2048;
 constexpr int kSoftWarps = 4;
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kThreads = kSoftThreads + 64;      // + the loading warp and the MMA warp
+constexpr int kThreads = kSoftThreads + 96;      // + the loading warp and the two MMA warps
 constexpr int kTmemO = 0;                        // 4 x 64 columns
 constexpr int kTmemS = 256;                      // 2 x 64 columns
 // A row's reference maximum follows its running maximum only when it falls behind by
@@ -60,7 +61,7 @@ struct Shared {
     uint64_t pair_full[kPairSlots], pair_empty[kPairSlots];
     uint64_t rope_full[kRopeSlots], rope_empty[kRopeSlots];
     uint64_t s_full[2], s_empty[2];
-    uint64_t p_full, pv_done, q_full, q_empty, mma_done;
+    uint64_t p_full, pv_done, q_full, q_empty, mma_done[2];
     uint32_t tmem;
     int abort;
     float factor[kRows];
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh.pv_done), 1);
         mbar_init(smem_u32(&sh.q_full), kSoftThreads);
         mbar_init(smem_u32(&sh.q_empty), 1);
-        mbar_init(smem_u32(&sh.mma_done), 1);
+        mbar_init(smem_u32(&sh.mma_done[0]), 1), mbar_init(smem_u32(&sh.mma_done[1]), 1);
         sh.abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&map_lat);
@@ -258,166 +259,159 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kSoftWarps) {
         // -------------------------------------------------------- loads
-        const uint64_t pol = policy_evict_first();
-        const int subs = kKeys / a.box_rows;   // boxes per key tile (one page each)
-        const int step = a.box_rows == 64 ? 2 : 1;
-        Walk w;
-        w.start(a, sh);
-        uint32_t tile = 0;
-        uint32_t used = 0, parity = 0;   // per slot (pairs, then rotary): loaded at all; last load's phase
-        bool ok = true;
-        while (ok && w.next(a)) {
-            const int n = w.tiles();
-            const int32_t *tab = a.table + static_cast<int64_t>(w.b) * a.table_st;
-            // the page of this lane's box, one tile ahead; a box past the last key reads
-            // zeros (its page lies past the cache)
-            auto page_of = [&](int k) -> int64_t {
-                const int64_t key = static_cast<int64_t>(k) * kKeys + lane * a.box_rows;
-                if (lane >= subs || key >= w.keys || k >= w.k1) return -1;
-                return tab[key / a.page_size];
-            };
-            int64_t page = page_of(w.k0);
-            for (int j = 0; j < n && ok; ++j, ++tile) {
-                const int k = w.k0 + j;
-                int64_t cur = page;
-                page = page_of(k + 1);
-                const int64_t key = static_cast<int64_t>(k) * kKeys + lane * a.box_rows;
-                const int row = static_cast<int>(key % a.page_size);
-                if (lane < subs && key < w.keys && (cur < 0 || cur >= a.num_pages)) {
-                    record_error(a.err, ERR_BAD_INDEX);
-                    cur = -1;
-                }
-                const int z = cur < 0 ? static_cast<int>(a.num_pages) : static_cast<int>(cur);
-                const uint32_t turn = tile >> 1;   // earlier uses of this half of the ring
-                for (int g = 0; g <= kGroups && ok; ++g) {
-                    const bool is_rope = g == kGroups;
-                    const int slot = is_rope ? tile & 1 : (tile & 1) * kGroups + g;
-                    const uint32_t full = smem_u32(is_rope ? &sh.rope_full[slot] : &sh.pair_full[slot]);
-                    const uint32_t empty = smem_u32(is_rope ? &sh.rope_empty[slot] : &sh.pair_empty[slot]);
-                    int got = 1;
-                    if (lane == 0) {
-                        got = wait(empty, (turn & 1) ^ 1, ERR_WAIT_SMEM_EMPTY);
-                        if (got) mbar_arrive_expect_tx(full, is_rope ? kGroupBytes : kPairBytes);
-                    }
-                    ok = __shfl_sync(0xffffffffu, got, 0);
-                    if (!ok) break;
-                    const int bit = is_rope ? kPairSlots + slot : slot;
-                    used |= 1u << bit;
-                    parity = (parity & ~(1u << bit)) | ((turn & 1) << bit);
-                    if (lane < subs) {
-                        const uint32_t dst = sbase + (is_rope ? kOffRope + slot * kGroupBytes : kOffPairs + slot * kPairBytes) +
-                                             lane * a.box_rows * 128;
-                        if (is_rope) {
-                            tma_load_4d(dst, &map_rope, full, 0, row, 2 * kGroups, z, pol);
-                        } else {
-                            for (int c = 0; c < 2; c += step)
-                                tma_load_4d(dst + c * kGroupBytes, &map_lat, full, 0, row, 2 * g + c, z, pol);
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
-            w.advance();
-        }
-        // the ring's last loads must land before the CTA may exit
-        if (lane == 0)
-            for (int i = 0; i < kPairSlots + kRopeSlots; ++i)
-                if (used >> i & 1)
-                    mbar_wait_drain(smem_u32(i < kPairSlots ? &sh.pair_full[i] : &sh.rope_full[i - kPairSlots]),
-                                    parity >> i & 1, a.err);
-        __syncwarp();
-    } else if (warp == kSoftWarps + 1) {
-        // -------------------------------------------------------- MMA issue
-        // Two queues, each in order: the scores' column groups as they arrive, and the
-        // second products as their weights are ready, which go first because they free
-        // the ring. Neither waits for the other: a thread that blocked on a key tile
-        // would keep back the product whose end lets that tile be loaded.
         if (elect_one()) {
-            constexpr uint32_t id_s = idesc16(E::kFmt, kRows, kKeys);
-            constexpr uint32_t id_o = idesc16(E::kFmt, 128, kRows, true, false);
-            const uint64_t dq = sdesc_sw128(sbase), dp = sdesc_sw128(sbase + kOffP);
-            const uint64_t dk = sdesc_sw128(sbase + kOffPairs), dr = sdesc_sw128(sbase + kOffRope);
-            const uint64_t dv = sdesc_mn_sw128(sbase + kOffPairs, kGroupBytes);
+            const uint64_t pol = policy_evict_first();
+            const int box = a.box_rows, subs = kKeys / box;   // boxes per key tile (one page each)
             Walk w;
             w.start(a, sh);
-            uint32_t s_tile = 0, p_tile = 0, seg = 0;   // tiles whose scores / products are next
+            uint32_t tile = 0;
+            uint32_t used = 0, parity = 0;   // per slot (pairs, then rotary): loaded at all; last load's phase
             bool ok = true;
             while (ok && w.next(a)) {
                 const int n = w.tiles();
-                if (n > 0) {
-                    ok = wait(smem_u32(&sh.q_full), seg & 1, ERR_WAIT_TMA_FULL);
-                    ++seg;
-                    tc_fence_after();
-                    const uint32_t s_end = s_tile + n, p_first = p_tile, p_end = p_tile + n;
-                    int g = 0;   // next column group of s_tile
-                    unsigned idle = 0;
-                    unsigned long long t0 = 0;
-                    while (ok && p_tile != p_end) {
-                        if (s_tile != p_tile && mbar_test(smem_u32(&sh.p_full), p_tile & 1)) {
-                            tc_fence_after();
-                            const uint32_t half = p_tile & 1, acc0 = p_tile != p_first;
+                const int32_t *tab = a.table + static_cast<int64_t>(w.b) * a.table_st;
+                // position of the next box whose page is fetched: one tile ahead of the loads
+                int key = w.k0 * kKeys, row = key % a.page_size;
+                const int end = min(w.keys, w.k1 * kKeys);
+                tab += key / a.page_size;
+                int page[kMaxSubs], at[kMaxSubs];
+                auto fetch = [&]() {
 #pragma unroll
-                            for (int m = 0; m < kGroups; ++m) {
-                                const uint64_t v = dv + ((half * kGroups + m) * kPairBytes >> 4);
+                    for (int i = 0; i < kMaxSubs; ++i) {
+                        if (i >= subs) break;
+                        at[i] = row;
+                        page[i] = key < end ? *tab : -1;
+                        key += box;
+                        row += box;
+                        if (row == a.page_size) row = 0, ++tab;
+                    }
+                };
+                if (n > 0) fetch();
+                for (int j = 0; j < n && ok; ++j, ++tile) {
+                    int z[kMaxSubs], y[kMaxSubs];
+                    const int live = min(subs, (w.keys - (w.k0 + j) * kKeys + box - 1) / box);
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma_16_ss(tmem + kTmemO + m * kRows, v + (k * 2048 >> 4), dp + (k * 32 >> 4), id_o,
-                                              k > 0 ? 1 : acc0);
-                                mma_commit(smem_u32(&sh.pair_empty[half * kGroups + m]));
-                            }
-                            mma_commit(smem_u32(&sh.pv_done));
-                            ++p_tile;
-                            idle = 0;
-                            continue;
-                        }
-                        if (s_tile != s_end) {
-                            const uint32_t buf = s_tile & 1, ph = (s_tile >> 1) & 1;
-                            const bool is_rope = g == kGroups;
-                            const int slot = is_rope ? buf : buf * kGroups + g;
-                            if ((g > 0 || mbar_test(smem_u32(&sh.s_empty[buf]), ph ^ 1)) &&
-                                mbar_test(smem_u32(is_rope ? &sh.rope_full[slot] : &sh.pair_full[slot]), ph)) {
-                                tc_fence_after();
-                                const uint32_t d = tmem + kTmemS + buf * kKeys;
-                                const uint64_t q = dq + (g * 2 * kRows * 128 >> 4);
-                                if (is_rope) {
-                                    const uint64_t k0 = dr + (slot * kGroupBytes >> 4);
+                    for (int i = 0; i < kMaxSubs; ++i) {
+                        if (i >= subs) break;
+                        // a box past the last key reads zeros (its page lies past the cache)
+                        const bool bad = static_cast<uint32_t>(page[i]) >= static_cast<uint32_t>(a.num_pages);
+                        if (bad && i < live) record_error(a.err, ERR_BAD_INDEX);
+                        z[i] = bad ? static_cast<int>(a.num_pages) : page[i];
+                        y[i] = at[i];
+                    }
+                    if (j + 1 < n) fetch();
+                    const uint32_t turn = tile >> 1;   // earlier uses of this half of the ring
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k) mma_16_ss(d, q + (k * 32 >> 4), k0 + (k * 32 >> 4), id_s, 1);
-                                    mma_commit(smem_u32(&sh.s_full[buf]));
-                                    mma_commit(smem_u32(&sh.rope_empty[buf]));
-                                    if (s_tile + 1 == s_end) mma_commit(smem_u32(&sh.q_empty));
-                                    ++s_tile;
-                                    g = 0;
-                                } else {
-                                    const uint64_t k0 = dk + (slot * kPairBytes >> 4);
-                                    const uint32_t acc0 = g > 0;
+                    for (int g = 0; g <= kGroups; ++g) {
+                        const bool is_rope = g == kGroups;
+                        const int slot = is_rope ? tile & 1 : (tile & 1) * kGroups + g;
+                        const uint32_t full = smem_u32(is_rope ? &sh.rope_full[slot] : &sh.pair_full[slot]);
+                        const uint32_t empty = smem_u32(is_rope ? &sh.rope_empty[slot] : &sh.pair_empty[slot]);
+                        if (!wait(empty, (turn & 1) ^ 1, ERR_WAIT_SMEM_EMPTY)) { ok = false; break; }
+                        mbar_arrive_expect_tx(full, is_rope ? kGroupBytes : kPairBytes);
+                        const int bit = is_rope ? kPairSlots + slot : slot;
+                        used |= 1u << bit;
+                        parity = (parity & ~(1u << bit)) | ((turn & 1) << bit);
+                        const uint32_t dst = sbase + (is_rope ? kOffRope + slot * kGroupBytes : kOffPairs + slot * kPairBytes);
+                        if (subs == 1) {
+                            tma_load_4d(dst, is_rope ? &map_rope : &map_lat, full, 0, y[0], 2 * g, z[0], pol);
+                        } else {
 #pragma unroll
-                                    for (int k = 0; k < 8; ++k)
-                                        mma_16_ss(d, q + ((k >> 2) * kRows * 128 + (k & 3) * 32 >> 4),
-                                                  k0 + ((k >> 2) * kGroupBytes + (k & 3) * 32 >> 4), id_s, k > 0 ? 1 : acc0);
-                                    ++g;
-                                }
-                                idle = 0;
-                                continue;
-                            }
-                        }
-                        // bounded: after the limit, or when another role gave up, leave
-                        if ((++idle & 1023u) == 0) {
-                            const unsigned long long t = globaltimer();
-                            if (idle == 1024u) t0 = t;
-                            if (ld_volatile_shared(wait.abort_addr)) ok = false;
-                            else if (t - t0 > kWaitLimitNs) {
-                                st_volatile_shared(wait.abort_addr, 1);
-                                record_error(a.err, ERR_WAIT_TMA_FULL);
-                                ok = false;
+                            for (int i = 0; i < kMaxSubs; ++i) {
+                                if (i >= subs) break;
+                                tma_load_4d(dst + i * box * 128, &map_rope, full, 0, y[i], 2 * g, z[i], pol);
+                                if (!is_rope)
+                                    tma_load_4d(dst + kGroupBytes + i * box * 128, &map_rope, full, 0, y[i], 2 * g + 1, z[i], pol);
                             }
                         }
                     }
                 }
                 w.advance();
             }
-            mma_commit(smem_u32(&sh.mma_done));
-            mbar_wait_drain(smem_u32(&sh.mma_done), 0, a.err);
+            // the ring's last loads must land before the CTA may exit
+            for (int i = 0; i < kPairSlots + kRopeSlots; ++i)
+                if (used >> i & 1)
+                    mbar_wait_drain(smem_u32(i < kPairSlots ? &sh.pair_full[i] : &sh.rope_full[i - kPairSlots]),
+                                    parity >> i & 1, a.err);
+        }
+        __syncwarp();
+    } else if (warp == kSoftWarps + 1) {
+        // -------------------------------------------------------- score MMAs
+        // The two products are issued by two warps that wait apart: one thread that
+        // blocked on a key tile would keep back the second product whose end lets that
+        // tile be loaded, and one that polled for either would spend 100 cycles, three
+        // small MMAs' time, on every test.
+        if (elect_one()) {
+            constexpr uint32_t id_s = idesc16(E::kFmt, kRows, kKeys);
+            const uint64_t dq = sdesc_sw128(sbase), dk = sdesc_sw128(sbase + kOffPairs), dr = sdesc_sw128(sbase + kOffRope);
+            Walk w;
+            w.start(a, sh);
+            uint32_t tile = 0, seg = 0;
+            bool ok = true;
+            while (ok && w.next(a)) {
+                const int n = w.tiles();
+                if (n > 0) {
+                    ok = wait(smem_u32(&sh.q_full), seg & 1, ERR_WAIT_TMA_FULL);
+                    ++seg;
+                }
+                for (int j = 0; j < n && ok; ++j, ++tile) {
+                    const uint32_t buf = tile & 1, ph = (tile >> 1) & 1, d = tmem + kTmemS + buf * kKeys;
+                    if (!wait(smem_u32(&sh.s_empty[buf]), ph ^ 1, ERR_WAIT_PART_EMPTY)) { ok = false; break; }
+#pragma unroll
+                    for (int g = 0; g <= kGroups; ++g) {
+                        const bool is_rope = g == kGroups;
+                        if (!wait(smem_u32(is_rope ? &sh.rope_full[buf] : &sh.pair_full[buf * kGroups + g]), ph, ERR_WAIT_TMA_FULL)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t q = dq + (g * 2 * kRows * 128 >> 4);
+                        const uint64_t k0 = is_rope ? dr + (buf * kGroupBytes >> 4) : dk + ((buf * kGroups + g) * kPairBytes >> 4);
+#pragma unroll
+                        for (int k = 0; k < (is_rope ? 4 : 8); ++k)
+                            mma_16_ss(d, q + ((k >> 2) * kRows * 128 + (k & 3) * 32 >> 4),
+                                      k0 + ((k >> 2) * kGroupBytes + (k & 3) * 32 >> 4), id_s, g > 0 || k > 0);
+                    }
+                    if (!ok) break;
+                    mma_commit(smem_u32(&sh.s_full[buf]));
+                    mma_commit(smem_u32(&sh.rope_empty[buf]));
+                    if (j + 1 == n) mma_commit(smem_u32(&sh.q_empty));
+                }
+                w.advance();
+            }
+            mma_commit(smem_u32(&sh.mma_done[0]));
+            mbar_wait_drain(smem_u32(&sh.mma_done[0]), 0, a.err);
+        }
+        __syncwarp();
+    } else if (warp == kSoftWarps + 2) {
+        // -------------------------------------------------------- weight x latent MMAs
+        if (elect_one()) {
+            constexpr uint32_t id_o = idesc16(E::kFmt, 128, kRows, true, false);
+            const uint64_t dp = sdesc_sw128(sbase + kOffP), dv = sdesc_mn_sw128(sbase + kOffPairs, kGroupBytes);
+            Walk w;
+            w.start(a, sh);
+            uint32_t tile = 0;
+            bool ok = true;
+            while (ok && w.next(a)) {
+                const int n = w.tiles();
+                for (int j = 0; j < n && ok; ++j, ++tile) {
+                    if (!wait(smem_u32(&sh.p_full), tile & 1, ERR_WAIT_PART_FULL)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t half = tile & 1, acc0 = j > 0;
+#pragma unroll
+                    for (int m = 0; m < kGroups; ++m) {
+                        const uint64_t v = dv + ((half * kGroups + m) * kPairBytes >> 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_16_ss(tmem + kTmemO + m * kRows, v + (k * 2048 >> 4), dp + (k * 32 >> 4), id_o, k > 0 ? 1 : acc0);
+                        mma_commit(smem_u32(&sh.pair_empty[half * kGroups + m]));
+                    }
+                    mma_commit(smem_u32(&sh.pv_done));
+                }
+                w.advance();
+            }
+            mma_commit(smem_u32(&sh.mma_done[1]));
+            mbar_wait_drain(smem_u32(&sh.mma_done[1]), 0, a.err);
         }
         __syncwarp();
     } else {
