@@ -100,6 +100,29 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
                  : "r"(taddr));
 }
 
+// 16 lanes x 32 columns in the 16x256b shape (tmem_ld_16x64, four 8-column groups).
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : MLA_R8(0), MLA_R8(8)
+        : "r"(taddr));
+}
+
+// Four 8x8 matrices of 16-bit values, stored transposed: lane 8i + j names the row that
+// receives column j of matrix i.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t src) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+    return v;
+}
+
 // The store counterpart of tmem_ld32.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], " MLA_LIST32_1 ";" ::"r"(taddr), MLA_W8(0), MLA_W8(8),
@@ -207,8 +230,6 @@ struct RopeArgs {
 };
 
 struct PagedArgs {
-    const void *q;            // [Tq, H, 576]
-    int64_t q_st, q_sh;
     int64_t Tq;
     const int32_t *table;     // [B, table_st]
     int64_t table_st;
@@ -219,6 +240,7 @@ struct PagedArgs {
     float *lse;               // [Tq, H] or NULL
     int64_t num_pages;
     int max_pages, page_size, box_rows;
+    int q_box;                // heads of one query load
     int B, H;
     float scale_log2;         // scale * log2(e)
     float *part_o;            // [2 * grid][64][512]
@@ -247,8 +269,8 @@ struct ProjArgs {
 };
 
 cudaError_t launch_rope(const RopeArgs &a, bool bf16, int num_sms, cudaStream_t stream);
-cudaError_t launch_paged(const CUtensorMap &latent, const CUtensorMap &rope, const PagedArgs &a, bool bf16, int grid,
-                         cudaStream_t stream);
+cudaError_t launch_paged(const CUtensorMap &q, const CUtensorMap &latent, const CUtensorMap &rope, const PagedArgs &a,
+                         bool bf16, int grid, cudaStream_t stream);
 cudaError_t launch_ragged(const CUtensorMap &q, const CUtensorMap &k_nope, const CUtensorMap &k_pe,
                           const CUtensorMap &v, const RaggedArgs &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_proj(const CUtensorMap &x, const CUtensorMap &w, const ProjArgs &a, bool bf16, bool w_kn,

@@ -1,5 +1,6 @@
 // C ABI of the latent attention (declared in include/moe_fp8.h): argument checks,
 // tensor maps and workspace layout.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -238,7 +239,7 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
     MLA_CHECK(ptr(workspace, "workspace"));
 
     PagedArgs a{};
-    a.q = q, a.q_st = q_st, a.q_sh = q_sh, a.Tq = Tq;
+    a.Tq = Tq;
     a.table = table, a.table_st = table_st, a.ctx = ctx, a.cu_q = cu_q;
     a.out = out, a.o_st = o_st, a.o_sh = o_sh, a.lse = lse;
     a.num_pages = num_pages, a.max_pages = max_pages, a.page_size = page_size;
@@ -255,6 +256,16 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
     a.joins = reinterpret_cast<int4 *>(ws);
     MLA_CUDA(device_error_word(&a.err), "error word address");
 
+    // the queries as (column of a 64-column group, head, group, token): one load takes the
+    // largest power-of-two share of the heads that also divides the 64 rows of a tile,
+    // so that loads start on multiples of it and never cross a token
+    a.q_box = std::min(64, H & -H);
+    CUtensorMap mq;
+    {
+        const int64_t d[4] = {64, H, kMlaWidth / 64, Tq}, s[3] = {q_sh, 64, q_st};
+        const int box[4] = {64, a.q_box, a.q_box == 64 ? kMlaWidth / 64 : 1, 1};
+        MLA_CHECK(tensor_map(&mq, q, dtype, 4, d, s, box, "q"));
+    }
     // the cache as (column of a 64-column group, row of a page, group, page): one load
     // takes box_rows rows of one group, or of two adjacent groups from 64-row pages
     CUtensorMap lat, rope;
@@ -264,7 +275,7 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
     const int box1[4] = {64, a.box_rows, 1, 1};
     MLA_CHECK(tensor_map(&lat, cache, dtype, 4, dims, strides, box2, "latents"));
     MLA_CHECK(tensor_map(&rope, cache, dtype, 4, dims, strides, box1, "rotary keys"));
-    MLA_CUDA(launch_paged(lat, rope, a, dtype == MLA_BF16, grid, static_cast<cudaStream_t>(stream)),
+    MLA_CUDA(launch_paged(mq, lat, rope, a, dtype == MLA_BF16, grid, static_cast<cudaStream_t>(stream)),
              "paged attention launch");
     report_launches(2);
     return MOE_OK;

@@ -44,7 +44,7 @@ constexpr int kOffMisc = kOffRope + kRopeSlots * kGroupBytes;
 constexpr int kSmem = kOffMisc + 2048;
 constexpr int kSoftWarps = 4;
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kThreads = kSoftThreads + 96;      // + the loading warp and the two MMA warps
+constexpr int kThreads = kSoftThreads + 128;     // + loads of keys and of queries, two MMA warps
 constexpr int kTmemO = 0;                        // 4 x 64 columns
 constexpr int kTmemS = 256;                      // 2 x 64 columns
 // A row's reference maximum follows its running maximum only when it falls behind by
@@ -67,8 +67,9 @@ struct Shared {
     float factor[kRows];
     int64_t row_off[kRows];
     int64_t warp_sum[kThreads / 32];
-    int64_t total, lo, hi, start_off;
-    int start_b, parts;
+    // the line of key tiles: CTA c's part starts at each * c + min(c, rem)
+    int64_t each, lo, hi, start_off;
+    int rem, start_b, start_rt;
 };
 static_assert(sizeof(Shared) <= 2048, "");
 
@@ -111,7 +112,7 @@ struct Walk {
     int k0, k1, kt, keys;
 
     __device__ void start(const PagedArgs &a, const Shared &sh) {
-        b = sh.start_b, rt = 0, at = sh.lo, hi = sh.hi, off = sh.start_off;
+        b = sh.start_b, rt = sh.start_rt, at = sh.lo, hi = sh.hi, off = sh.start_off;
         s = read_seq(a, b, false);
         rts = row_tiles(s, a.H);
     }
@@ -149,7 +150,13 @@ struct Walk {
     __device__ int tiles() const { return keys > 0 ? k1 - k0 : 0; }
 };
 
-__device__ __forceinline__ int64_t part_lo(int64_t total, int parts, int c) { return total * c / parts; }
+__device__ __forceinline__ int64_t part_lo(int64_t each, int rem, int c) { return each * c + min(c, rem); }
+
+// The CTA whose part holds unit u.
+__device__ __forceinline__ int part_of(int64_t each, int rem, int64_t u) {
+    const int64_t longer = (each + 1) * rem;
+    return static_cast<int>(u < longer ? u / (each + 1) : rem + (u - longer) / each);
+}
 
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 #pragma unroll
@@ -164,6 +171,7 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t base = 0;
+    if (tid == 0) sh.start_b = 0, sh.start_rt = 0, sh.start_off = 0;   // a CTA without a part starts nowhere else
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
         Seq s{0, 0, 0};
@@ -200,32 +208,53 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
         base += all;
         __syncthreads();
     }
-    if (tid == 0) {
-        const int64_t most = (base + kMinTiles - 1) / kMinTiles;
-        const int parts = most < 1 ? 1 : most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
-        const int c = blockIdx.x;
-        sh.total = base;
-        sh.parts = parts;
-        sh.lo = c < parts ? part_lo(base, parts, c) : base;
-        sh.hi = c < parts ? part_lo(base, parts, c + 1) : base;
-        sh.start_b = 0;
-        sh.start_off = 0;
+    const int64_t most = base / kMinTiles;
+    const unsigned parts = most < 1 ? 1u : most < gridDim.x ? static_cast<unsigned>(most) : gridDim.x;
+    int64_t each;
+    int rem;
+    if (base < (int64_t{1} << 32)) {   // 32-bit division takes a quarter of the time
+        const unsigned t = static_cast<unsigned>(base);
+        each = t / parts, rem = static_cast<int>(t % parts);
+    } else {
+        each = base / parts, rem = static_cast<int>(base % parts);
     }
-    __syncthreads();
-    if (sh.lo < sh.hi)
-        for (int b = tid; b < a.B; b += kThreads) {
-            const int64_t p = prefix[b], e = b + 1 < a.B ? prefix[b + 1] : sh.total;
-            if (p <= sh.lo && sh.lo < e) {
-                sh.start_b = b;
-                sh.start_off = sh.lo - p;
-            }
+    const unsigned c = blockIdx.x;
+    const int64_t lo = c < parts ? part_lo(each, rem, c) : base, hi = c < parts ? part_lo(each, rem, c + 1) : base;
+    if (tid == 0) sh.each = each, sh.rem = rem, sh.lo = lo, sh.hi = hi;
+    for (int b = tid; b < a.B; b += kThreads) {
+        const int64_t p = prefix[b], e = b + 1 < a.B ? prefix[b + 1] : base;
+        if (p <= lo && lo < e) {
+            sh.start_b = b;
+            sh.start_rt = 0;
+            sh.start_off = lo - p;
         }
+    }
+    fence_async_smem();   // the prefixes' buffer is filled by TMA next
+    __syncthreads();
+    if (warp == 0 && lo < hi) {
+        // the row tile of that sequence: 32 at a time
+        const Seq s = read_seq(a, sh.start_b, false);
+        const int rts = row_tiles(s, a.H);
+        int64_t off = sh.start_off;
+        for (int r0 = 0; r0 < rts; r0 += 32) {
+            const int64_t u = r0 + lane < rts ? units_of(tile_keys(s, r0 + lane, a.H)) : 0;
+            const int64_t inc = warp_scan(u, lane);
+            if (inc - u <= off && off < inc) {
+                sh.start_rt = r0 + lane;
+                sh.start_off = off - (inc - u);
+            }
+            const int64_t all = __shfl_sync(0xffffffffu, inc, 31);
+            if (off < all) break;
+            off -= all;
+        }
+    }
     __syncthreads();
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_attn_kernel(const __grid_constant__ CUtensorMap map_lat, const __grid_constant__ CUtensorMap map_rope,
+    paged_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_lat,
+                      const __grid_constant__ CUtensorMap map_rope,
                       const PagedArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem + kOffMisc);
@@ -240,11 +269,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.s_full[i]), 1), mbar_init(smem_u32(&sh.s_empty[i]), kSoftThreads);
         mbar_init(smem_u32(&sh.p_full), kSoftThreads);
         mbar_init(smem_u32(&sh.pv_done), 1);
-        mbar_init(smem_u32(&sh.q_full), kSoftThreads);
+        mbar_init(smem_u32(&sh.q_full), 1);
         mbar_init(smem_u32(&sh.q_empty), 1);
         mbar_init(smem_u32(&sh.mma_done[0]), 1), mbar_init(smem_u32(&sh.mma_done[1]), 1);
         sh.abort = 0;
         fence_barrier_init();
+        tma_prefetch_desc(&map_q);
         tma_prefetch_desc(&map_lat);
         tma_prefetch_desc(&map_rope);
     }
@@ -335,6 +365,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     parity >> i & 1, a.err);
         }
         __syncwarp();
+    } else if (warp == kSoftWarps + 3) {
+        // -------------------------------------------------------- queries
+        // Apart from the keys, which run ahead of the segment: the next segment's rows
+        // replace this one's as soon as its last scores are done.
+        if (elect_one()) {
+            const uint64_t pol = policy_evict_normal();
+            Walk w;
+            w.start(a, sh);
+            uint32_t seg = 0;
+            bool ok = true;
+            while (ok && w.next(a)) {
+                if (w.tiles() > 0) {
+                    const uint32_t full = smem_u32(&sh.q_full);
+                    if (!wait(smem_u32(&sh.q_empty), (seg & 1) ^ 1, ERR_WAIT_SMEM_EMPTY)) break;
+                    mbar_arrive_expect_tx(full, kQBytes);
+                    const int r0 = w.rt * kRows;
+                    int t = r0 / a.H, h = r0 - t * a.H;
+                    for (int r = 0; r < kRows; r += a.q_box) {
+                        // rows past the sequence are the next one's (or zero): computed, not kept
+                        if (a.q_box == kRows) {
+                            tma_load_4d(sbase, &map_q, full, 0, h, 0, w.s.row0 + t, pol);
+                        } else {
+                            for (int c = 0; c < kMlaWidth / 64; ++c)
+                                tma_load_4d(sbase + (c * kRows + r) * 128, &map_q, full, 0, h, c, w.s.row0 + t, pol);
+                        }
+                        h += a.q_box;
+                        if (h >= a.H) h = 0, ++t;
+                    }
+                    ++seg;
+                }
+                w.advance();
+            }
+            if (seg > 0) mbar_wait_drain(smem_u32(&sh.q_full), (seg - 1) & 1, a.err);
+        }
+        __syncwarp();
     } else if (warp == kSoftWarps + 1) {
         // -------------------------------------------------------- score MMAs
         // The two products are issued by two warps that wait apart: one thread that
@@ -423,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c0 = 2 * (lane & 3);
         Walk w;
         w.start(a, sh);
-        uint32_t tile = 0, seg = 0;
+        uint32_t tile = 0;
         int4 join = make_int4(0, 0, 0, 0);
         // after a wait that gave up a thread waits no more but keeps to the loops, so
         // that every named barrier still gets all of its threads
@@ -441,32 +506,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const int vis_a = visible(ra), vis_b = visible(rb);
             float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
-            if (n > 0) {
-                // Q into shared memory (128-byte swizzle); rows past the sequence are zero
-                if (seg > 0) hold(&sh.q_empty, (seg - 1) & 1, ERR_WAIT_PART_EMPTY);
-                {
-                    // eight threads take a row's 72 vectors, 16 rows at a time
-                    const T *src[kRows / 16];
-#pragma unroll
-                    for (int i = 0; i < kRows / 16; ++i) {
-                        const int r = tid / 8 + 16 * i, t = (r0 + r) / a.H, h = r0 + r - t * a.H;
-                        src[i] = r < rows ? static_cast<const T *>(a.q) + (w.s.row0 + t) * a.q_st + h * a.q_sh : nullptr;
-                    }
-#pragma unroll
-                    for (int c = 0; c < kMlaWidth / 64; ++c)
-#pragma unroll
-                        for (int i = 0; i < kRows / 16; ++i) {
-                            const int r = tid / 8 + 16 * i, v = tid & 7;
-                            const uint32_t dst = sbase + c * kRows * 128 + r * 128 + ((v ^ (r & 7)) << 4);
-                            if (src[i]) cp_async_16(dst, src[i] + c * 64 + v * 8);
-                            else st_shared_v4(dst, make_uint4(0, 0, 0, 0));
-                        }
-                }
-                cp_async_wait_all();
-                fence_async_smem();
-                mbar_arrive(smem_u32(&sh.q_full));
-                ++seg;
-            }
             for (int j = 0; j < n; ++j, ++tile) {
                 const uint32_t buf = tile & 1, ph = (tile >> 1) & 1;
                 hold(&sh.s_full[buf], ph, ERR_WAIT_PART_FULL);
@@ -581,38 +620,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                 hold(&sh.pv_done, (tile - 1) & 1, ERR_WAIT_PART_FULL);
                 tc_fence_after();
             }
-            T *out = static_cast<T *>(a.out);
-            float *part = a.part_o + static_cast<int64_t>(slot) * kRows * kMlaLatent;
-            for (int c = 0; c < kGroups * kRows; c += 32) {
-                uint32_t o[32];
-                if (n > 0) {
-                    tmem_ld32(tmem + kTmemO + c + lane_base, o);
-                    tmem_wait_ld();
-                } else {
+            if (whole) {
+                // O^T (lanes: columns of the latent; columns: rows) leaves transposed, 32
+                // rows x 32 latent columns of a warp at a time, through the warp's own 2 KB
+                // of the weights' buffer: 16-byte stores, 64 bytes of a row per four lanes
+                const uint32_t stage = sbase + kOffP + warp * 2048;
+                const uint32_t st_row = lane & 7, st_chunk = lane >> 3;
+                T *out = static_cast<T *>(a.out) + warp * 32 + (lane & 3) * 8;
+                for (int c = 0; c < kGroups * kRows; c += 32) {
+                    uint32_t o0[16], o1[16];
+                    if (n > 0) {
+                        tmem_ld_16x32(tmem + kTmemO + c + lane_base, o0);
+                        tmem_ld_16x32(tmem + kTmemO + c + lane_base + (16u << 16), o1);
+                        tmem_wait_ld();
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0;
-                }
-                const int dim = (c / kRows) * 128 + warp * 32 + lane;
-                const int rbase = c & 32;
-                if (whole) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int64_t off = sh.row_off[rbase + i];
-                        if (off >= 0) out[off + dim] = E::from(__uint_as_float(o[i]) * sh.factor[rbase + i]);
+                        for (int i = 0; i < 16; ++i) o0[i] = o1[i] = 0;
                     }
-                } else {
+                    const int rbase = c & 32;
+                    __syncwarp();   // the last 32 rows have been read
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float2 f = *reinterpret_cast<const float2 *>(&sh.factor[rbase + 8 * g + c0]);
+                        auto two = [&](const uint32_t *o) { return E::pack(__uint_as_float(o[0]) * f.x, __uint_as_float(o[1]) * f.y); };
+                        // rows of 64 bytes; the 16-byte unit is swizzled by the row pair
+                        stmatrix_x4_trans(stage + (8 * g + st_row) * 64 + ((st_chunk ^ (st_row >> 1)) << 4), two(o0 + 4 * g),
+                                          two(o0 + 4 * g + 2), two(o1 + 4 * g), two(o1 + 4 * g + 2));
+                    }
+                    __syncwarp();
+                    T *dst = out + (c / kRows) * 128;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int r = 8 * g + (lane >> 2);
+                        const int64_t off = sh.row_off[rbase + r];
+                        const uint4 v = ld_shared_v4(stage + r * 64 + (((lane & 3) ^ ((r & 7) >> 1)) << 4));
+                        if (off >= 0) *reinterpret_cast<uint4 *>(dst + off) = v;
+                    }
+                }
+            } else {
+                float *part = a.part_o + static_cast<int64_t>(slot) * kRows * kMlaLatent + warp * 32 + lane;
+                for (int c = 0; c < kGroups * kRows; c += 32) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tmem_ld32(tmem + kTmemO + c + lane_base, o);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0;
+                    }
+                    const int rbase = c & 32;
+                    float *dst = part + rbase * kMlaLatent + (c / kRows) * 128;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (rbase + i < rows) part[(rbase + i) * kMlaLatent + dim] = __uint_as_float(o[i]);
+                        if (rbase + i < rows) dst[i * kMlaLatent] = __uint_as_float(o[i]);
                 }
             }
             tc_fence_before();
             if (!whole && w.k0 == 0) {
                 // this CTA holds the item's first key tiles: it names the item to the join
-                const int64_t last = w.at + (w.kt - 1);
-                int64_t c_end = blockIdx.x;
-                while (part_lo(sh.total, sh.parts, static_cast<int>(c_end) + 1) <= last) ++c_end;
-                join = make_int4(w.s.row0, r0, rows, static_cast<int>(c_end));
+                const int c_end = part_of(sh.each, sh.rem, w.at + (w.kt - 1));
+                join = make_int4(w.s.row0, r0, rows, c_end);
             }
             w.advance();
         }
@@ -738,22 +805,23 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
 }
 
 template <typename T>
-cudaError_t launch_t(const CUtensorMap &lat, const CUtensorMap &rope, const PagedArgs &a, int grid, cudaStream_t stream) {
+cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &lat, const CUtensorMap &rope, const PagedArgs &a, int grid,
+                     cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(paged_attn_kernel<T>, kSmem, done);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(paged_attn_kernel<T>, dim3(grid), dim3(kThreads), kSmem, stream, lat, rope, a);
+    e = launch_pdl(paged_attn_kernel<T>, dim3(grid), dim3(kThreads), kSmem, stream, q, lat, rope, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(paged_join_kernel<T>, dim3(2 * grid), dim3(kJoinThreads), 0, stream, a, grid);
 }
 
 }  // namespace
 
-cudaError_t launch_paged(const CUtensorMap &latent, const CUtensorMap &rope, const PagedArgs &a, bool bf16, int grid,
-                         cudaStream_t stream) {
+cudaError_t launch_paged(const CUtensorMap &q, const CUtensorMap &latent, const CUtensorMap &rope, const PagedArgs &a,
+                         bool bf16, int grid, cudaStream_t stream) {
     if (grid > kMaxCtas) return cudaErrorInvalidValue;
-    return bf16 ? launch_t<__nv_bfloat16>(latent, rope, a, grid, stream)
-                : launch_t<__half>(latent, rope, a, grid, stream);
+    return bf16 ? launch_t<__nv_bfloat16>(q, latent, rope, a, grid, stream)
+                : launch_t<__half>(q, latent, rope, a, grid, stream);
 }
 
 }  // namespace moe
