@@ -156,11 +156,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// 16-byte asynchronous global -> shared copy (bypassing L1).
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
 __device__ __forceinline__ void st_shared_v4(uint32_t dst, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -269,8 +264,13 @@ struct ProjArgs {
 };
 
 cudaError_t launch_rope(const RopeArgs &a, bool bf16, int num_sms, cudaStream_t stream);
-cudaError_t launch_paged(const CUtensorMap &q, const CUtensorMap &latent, const CUtensorMap &rope, const PagedArgs &a,
-                         bool bf16, int grid, cudaStream_t stream);
+// Tensor maps of mla_attn_paged: the queries; the cache in loads of two column groups
+// and of one.
+struct PagedMaps {
+    CUtensorMap q, pair, group;
+};
+
+cudaError_t launch_paged(const PagedMaps &m, const PagedArgs &a, bool bf16, int grid, cudaStream_t stream);
 cudaError_t launch_ragged(const CUtensorMap &q, const CUtensorMap &k_nope, const CUtensorMap &k_pe,
                           const CUtensorMap &v, const RaggedArgs &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_proj(const CUtensorMap &x, const CUtensorMap &w, const ProjArgs &a, bool bf16, bool w_kn,

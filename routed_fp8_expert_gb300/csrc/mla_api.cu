@@ -260,23 +260,20 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
     // largest power-of-two share of the heads that also divides the 64 rows of a tile,
     // so that loads start on multiples of it and never cross a token
     a.q_box = std::min(64, H & -H);
-    CUtensorMap mq;
+    PagedMaps m;
     {
         const int64_t d[4] = {64, H, kMlaWidth / 64, Tq}, s[3] = {q_sh, 64, q_st};
         const int box[4] = {64, a.q_box, a.q_box == 64 ? kMlaWidth / 64 : 1, 1};
-        MLA_CHECK(tensor_map(&mq, q, dtype, 4, d, s, box, "q"));
+        MLA_CHECK(tensor_map(&m.q, q, dtype, 4, d, s, box, "q"));
     }
-    // the cache as (column of a 64-column group, row of a page, group, page): one load
-    // takes box_rows rows of one group, or of two adjacent groups from 64-row pages
-    CUtensorMap lat, rope;
+    // the cache as (column of a 64-column group, row of a page, group, page)
     const int64_t dims[4] = {64, page_size, kMlaWidth / 64, num_pages};
     const int64_t strides[3] = {row_st, 64, page_st};
-    const int box2[4] = {64, a.box_rows, 2, 1};
-    const int box1[4] = {64, a.box_rows, 1, 1};
-    MLA_CHECK(tensor_map(&lat, cache, dtype, 4, dims, strides, box2, "latents"));
-    MLA_CHECK(tensor_map(&rope, cache, dtype, 4, dims, strides, box1, "rotary keys"));
-    MLA_CUDA(launch_paged(mq, lat, rope, a, dtype == MLA_BF16, grid, static_cast<cudaStream_t>(stream)),
-             "paged attention launch");
+    for (int groups : {1, 2}) {
+        const int box[4] = {64, a.box_rows, groups, 1};
+        MLA_CHECK(tensor_map(groups == 1 ? &m.group : &m.pair, cache, dtype, 4, dims, strides, box, "cache"));
+    }
+    MLA_CUDA(launch_paged(m, a, dtype == MLA_BF16, grid, static_cast<cudaStream_t>(stream)), "paged attention launch");
     report_launches(2);
     return MOE_OK;
 }

@@ -42,7 +42,7 @@ constexpr int kOffPairs = kOffP + kRows * 128;
 constexpr int kOffRope = kOffPairs + kPairSlots * kPairBytes;
 constexpr int kOffMisc = kOffRope + kRopeSlots * kGroupBytes;
 constexpr int kSmem = kOffMisc + 2048;
-constexpr int kSoftWarps = 4;
+constexpr int kSoftWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kThreads = kSoftThreads + 128;     // + loads of keys and of queries, two MMA warps
 constexpr int kTmemO = 0;                        // 4 x 64 columns
@@ -51,6 +51,7 @@ constexpr int kTmemS = 256;                      // 2 x 64 columns
 // more than 2^8: the sums then stay below 2^8 times their true scale, far from
 // overflow, and O is rescaled a few times per item instead of once per tile.
 constexpr float kLag = 8.0f;
+constexpr int kNoPage = -0x7fffffff - 1;
 // Fewest key tiles a CTA is given: below it the partial sums cost more than the split gains.
 constexpr int kMinTiles = 2;
 
@@ -64,7 +65,7 @@ struct Shared {
     uint64_t p_full, pv_done, q_full, q_empty, mma_done[2];
     uint32_t tmem;
     int abort;
-    float factor[kRows];
+    float factor[kRows], half_of[2][kRows];
     int64_t row_off[kRows];
     int64_t warp_sum[kThreads / 32];
     // the line of key tiles: CTA c's part starts at each * c + min(c, rem)
@@ -148,6 +149,47 @@ struct Walk {
     }
     // key tiles of the segment that hold keys
     __device__ int tiles() const { return keys > 0 ? k1 - k0 : 0; }
+};
+
+// Walks the same part key tile by key tile and reads the page table one tile ahead of
+// its user: page[i], row[i] of the boxes of the present tile (kNoPage past the last key).
+struct Cursor {
+    Walk w;
+    const int32_t *tab;
+    int j, n, key, at, end;
+    int page[kMaxSubs], row[kMaxSubs];
+
+    __device__ void start(const PagedArgs &a, const Shared &sh) {
+        w.start(a, sh);
+        j = n = 0;
+    }
+    __device__ bool step(const PagedArgs &a) {
+        if (j == n) {
+            do {
+                if (n > 0) w.advance();
+                n = 0;
+                if (!w.next(a)) return false;
+                n = w.tiles();
+                if (n == 0) w.advance();
+            } while (n == 0);
+            j = 0;
+            key = w.k0 * kKeys;
+            at = key % a.page_size;
+            end = min(w.keys, w.k1 * kKeys);
+            tab = a.table + static_cast<int64_t>(w.b) * a.table_st + key / a.page_size;
+        }
+        ++j;
+#pragma unroll
+        for (int i = 0; i < kMaxSubs; ++i) {
+            if (i * a.box_rows >= kKeys) break;
+            row[i] = at;
+            page[i] = key < end ? *tab : kNoPage;
+            key += a.box_rows;
+            at += a.box_rows;
+            if (at == a.page_size) at = 0, ++tab;
+        }
+        return true;
+    }
 };
 
 __device__ __forceinline__ int64_t part_lo(int64_t each, int rem, int c) { return each * c + min(c, rem); }
@@ -253,9 +295,7 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_lat,
-                      const __grid_constant__ CUtensorMap map_rope,
-                      const PagedArgs a) {
+    paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem + kOffMisc);
     const uint32_t sbase = smem_u32(smem);
@@ -274,9 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh.mma_done[0]), 1), mbar_init(smem_u32(&sh.mma_done[1]), 1);
         sh.abort = 0;
         fence_barrier_init();
-        tma_prefetch_desc(&map_q);
-        tma_prefetch_desc(&map_lat);
-        tma_prefetch_desc(&map_rope);
+        tma_prefetch_desc(&maps.q);
+        tma_prefetch_desc(&maps.pair);
+        tma_prefetch_desc(&maps.group);
     }
     if (warp == kSoftWarps + 1) tmem_alloc<512>(smem_u32(&sh.tmem));
     pdl_wait();
@@ -291,72 +331,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         // -------------------------------------------------------- loads
         if (elect_one()) {
             const uint64_t pol = policy_evict_first();
-            const int box = a.box_rows, subs = kKeys / box;   // boxes per key tile (one page each)
-            Walk w;
-            w.start(a, sh);
+            const int box = a.box_rows, subs = kKeys / box;
+            Cursor cur;
+            cur.start(a, sh);
+            bool more = cur.step(a);
             uint32_t tile = 0;
             uint32_t used = 0, parity = 0;   // per slot (pairs, then rotary): loaded at all; last load's phase
             bool ok = true;
-            while (ok && w.next(a)) {
-                const int n = w.tiles();
-                const int32_t *tab = a.table + static_cast<int64_t>(w.b) * a.table_st;
-                // position of the next box whose page is fetched: one tile ahead of the loads
-                int key = w.k0 * kKeys, row = key % a.page_size;
-                const int end = min(w.keys, w.k1 * kKeys);
-                tab += key / a.page_size;
-                int page[kMaxSubs], at[kMaxSubs];
-                auto fetch = [&]() {
+            while (ok && more) {
+                int z[kMaxSubs], y[kMaxSubs];
 #pragma unroll
-                    for (int i = 0; i < kMaxSubs; ++i) {
-                        if (i >= subs) break;
-                        at[i] = row;
-                        page[i] = key < end ? *tab : -1;
-                        key += box;
-                        row += box;
-                        if (row == a.page_size) row = 0, ++tab;
-                    }
-                };
-                if (n > 0) fetch();
-                for (int j = 0; j < n && ok; ++j, ++tile) {
-                    int z[kMaxSubs], y[kMaxSubs];
-                    const int live = min(subs, (w.keys - (w.k0 + j) * kKeys + box - 1) / box);
+                for (int i = 0; i < kMaxSubs; ++i) {
+                    if (i >= subs) break;
+                    // a box past the last key reads zeros (its page lies past the cache)
+                    const bool bad = static_cast<uint32_t>(cur.page[i]) >= static_cast<uint32_t>(a.num_pages);
+                    if (bad && cur.page[i] != kNoPage) record_error(a.err, ERR_BAD_INDEX);
+                    z[i] = bad ? static_cast<int>(a.num_pages) : cur.page[i];
+                    y[i] = cur.row[i];
+                }
+                more = cur.step(a);
+                const uint32_t turn = tile >> 1;   // earlier uses of this half of the ring
 #pragma unroll
-                    for (int i = 0; i < kMaxSubs; ++i) {
-                        if (i >= subs) break;
-                        // a box past the last key reads zeros (its page lies past the cache)
-                        const bool bad = static_cast<uint32_t>(page[i]) >= static_cast<uint32_t>(a.num_pages);
-                        if (bad && i < live) record_error(a.err, ERR_BAD_INDEX);
-                        z[i] = bad ? static_cast<int>(a.num_pages) : page[i];
-                        y[i] = at[i];
-                    }
-                    if (j + 1 < n) fetch();
-                    const uint32_t turn = tile >> 1;   // earlier uses of this half of the ring
+                for (int g = 0; g <= kGroups; ++g) {
+                    const bool is_rope = g == kGroups;
+                    const int slot = is_rope ? tile & 1 : (tile & 1) * kGroups + g;
+                    const uint32_t full = smem_u32(is_rope ? &sh.rope_full[slot] : &sh.pair_full[slot]);
+                    const uint32_t empty = smem_u32(is_rope ? &sh.rope_empty[slot] : &sh.pair_empty[slot]);
+                    if (!wait(empty, (turn & 1) ^ 1, ERR_WAIT_SMEM_EMPTY)) { ok = false; break; }
+                    mbar_arrive_expect_tx(full, is_rope ? kGroupBytes : kPairBytes);
+                    const int bit = is_rope ? kPairSlots + slot : slot;
+                    used |= 1u << bit;
+                    parity = (parity & ~(1u << bit)) | ((turn & 1) << bit);
+                    const uint32_t dst = sbase + (is_rope ? kOffRope + slot * kGroupBytes : kOffPairs + slot * kPairBytes);
+                    if (subs == 1) {
+                        tma_load_4d(dst, is_rope ? &maps.group : &maps.pair, full, 0, y[0], 2 * g, z[0], pol);
+                    } else {
 #pragma unroll
-                    for (int g = 0; g <= kGroups; ++g) {
-                        const bool is_rope = g == kGroups;
-                        const int slot = is_rope ? tile & 1 : (tile & 1) * kGroups + g;
-                        const uint32_t full = smem_u32(is_rope ? &sh.rope_full[slot] : &sh.pair_full[slot]);
-                        const uint32_t empty = smem_u32(is_rope ? &sh.rope_empty[slot] : &sh.pair_empty[slot]);
-                        if (!wait(empty, (turn & 1) ^ 1, ERR_WAIT_SMEM_EMPTY)) { ok = false; break; }
-                        mbar_arrive_expect_tx(full, is_rope ? kGroupBytes : kPairBytes);
-                        const int bit = is_rope ? kPairSlots + slot : slot;
-                        used |= 1u << bit;
-                        parity = (parity & ~(1u << bit)) | ((turn & 1) << bit);
-                        const uint32_t dst = sbase + (is_rope ? kOffRope + slot * kGroupBytes : kOffPairs + slot * kPairBytes);
-                        if (subs == 1) {
-                            tma_load_4d(dst, is_rope ? &map_rope : &map_lat, full, 0, y[0], 2 * g, z[0], pol);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < kMaxSubs; ++i) {
-                                if (i >= subs) break;
-                                tma_load_4d(dst + i * box * 128, &map_rope, full, 0, y[i], 2 * g, z[i], pol);
-                                if (!is_rope)
-                                    tma_load_4d(dst + kGroupBytes + i * box * 128, &map_rope, full, 0, y[i], 2 * g + 1, z[i], pol);
-                            }
+                        for (int i = 0; i < kMaxSubs; ++i) {
+                            if (i >= subs) break;
+                            tma_load_4d(dst + i * box * 128, &maps.group, full, 0, y[i], 2 * g, z[i], pol);
+                            if (!is_rope)
+                                tma_load_4d(dst + kGroupBytes + i * box * 128, &maps.group, full, 0, y[i], 2 * g + 1, z[i], pol);
                         }
                     }
                 }
-                w.advance();
+                ++tile;
             }
             // the ring's last loads must land before the CTA may exit
             for (int i = 0; i < kPairSlots + kRopeSlots; ++i)
@@ -385,10 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int r = 0; r < kRows; r += a.q_box) {
                         // rows past the sequence are the next one's (or zero): computed, not kept
                         if (a.q_box == kRows) {
-                            tma_load_4d(sbase, &map_q, full, 0, h, 0, w.s.row0 + t, pol);
+                            tma_load_4d(sbase, &maps.q, full, 0, h, 0, w.s.row0 + t, pol);
                         } else {
                             for (int c = 0; c < kMlaWidth / 64; ++c)
-                                tma_load_4d(sbase + (c * kRows + r) * 128, &map_q, full, 0, h, c, w.s.row0 + t, pol);
+                                tma_load_4d(sbase + (c * kRows + r) * 128, &maps.q, full, 0, h, c, w.s.row0 + t, pol);
                         }
                         h += a.q_box;
                         if (h >= a.H) h = 0, ++t;
@@ -481,10 +500,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------- softmax and results
-        const int tid = threadIdx.x;
-        const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-        // this thread's two rows of the tile and its 16 key columns (pairs of two)
-        const int ra = warp * 16 + lane / 4, rb = ra + 8;
+        // Eight warps: warps w and w + 4 hold the same 16 rows (a warp reaches the tensor
+        // memory lanes of its number modulo 4) and half of the tile's keys each, later
+        // half of the latent columns each.
+        const int tid = threadIdx.x, quad = warp & 3, half = warp >> 2;
+        const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+        // this thread's two rows of the tile and its 8 key columns (pairs of two)
+        const int ra = quad * 16 + lane / 4, rb = ra + 8;
         const int c0 = 2 * (lane & 3);
         Walk w;
         w.start(a, sh);
@@ -510,42 +532,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t buf = tile & 1, ph = (tile >> 1) & 1;
                 hold(&sh.s_full[buf], ph, ERR_WAIT_PART_FULL);
                 tc_fence_after();
-                uint32_t r[32];
-                tmem_ld_16x64(tmem + kTmemS + buf * kKeys + lane_base, r);
+                uint32_t r[16];
+                tmem_ld_16x32(tmem + kTmemS + buf * kKeys + half * 32 + lane_base, r);
                 tmem_wait_ld();
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sh.s_empty[buf]));
                 const int kb = (w.k0 + j) * kKeys;
+                if (kb + kKeys > min(vis_a, vis_b)) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = kb + half * 32 + 8 * g + c0 + e;
+                            if (key >= vis_a) r[4 * g + e] = __float_as_uint(-INFINITY);
+                            if (key >= vis_b) r[4 * g + 2 + e] = __float_as_uint(-INFINITY);
+                        }
+                }
                 float mx_a = -INFINITY, mx_b = -INFINITY;
 #pragma unroll
-                for (int g = 0; g < 8; ++g)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int key = kb + 8 * g + c0 + e;
-                        const float sa = key < vis_a ? __uint_as_float(r[4 * g + e]) * a.scale_log2 : -INFINITY;
-                        const float sb = key < vis_b ? __uint_as_float(r[4 * g + 2 + e]) * a.scale_log2 : -INFINITY;
-                        r[4 * g + e] = __float_as_uint(sa);
-                        r[4 * g + 2 + e] = __float_as_uint(sb);
-                        mx_a = fmaxf(mx_a, sa);
-                        mx_b = fmaxf(mx_b, sb);
-                    }
+                for (int g = 0; g < 4; ++g) {
+                    mx_a = fmaxf(mx_a, fmaxf(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1])));
+                    mx_b = fmaxf(mx_b, fmaxf(__uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3])));
+                }
 #pragma unroll
                 for (int o = 1; o < 4; o <<= 1) {
                     mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, o));
                     mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, o));
                 }
+                mx_a *= a.scale_log2, mx_b *= a.scale_log2;
                 const bool behind = mx_a > m_a + kLag || mx_b > m_b + kLag;
                 if (named_bar_or(1, kSoftThreads, behind)) {
-                    const float na = fmaxf(m_a, mx_a), nb = fmaxf(m_b, mx_b);
+                    if ((lane & 3) == 0) sh.half_of[half][ra] = mx_a, sh.half_of[half][rb] = mx_b;
+                    named_bar_sync(1, kSoftThreads);
+                    const float na = fmaxf(m_a, fmaxf(mx_a, sh.half_of[half ^ 1][ra]));
+                    const float nb = fmaxf(m_b, fmaxf(mx_b, sh.half_of[half ^ 1][rb]));
                     const float fa = m_a == -INFINITY ? 0.f : ex2(m_a - na), fb = m_b == -INFINITY ? 0.f : ex2(m_b - nb);
                     l_a *= fa, l_b *= fb;
                     m_a = na, m_b = nb;
                     if (j > 0) {
-                        if ((lane & 3) == 0) sh.factor[ra] = fa, sh.factor[rb] = fb;
+                        if (half == 0 && (lane & 3) == 0) sh.factor[ra] = fa, sh.factor[rb] = fb;
                         hold(&sh.pv_done, (tile - 1) & 1, ERR_WAIT_PART_FULL);
                         tc_fence_after();
                         named_bar_sync(1, kSoftThreads);
-                        for (int c = 0; c < kGroups * kRows; c += 32) {
+                        for (int c = half * 2 * kRows; c < (half + 1) * 2 * kRows; c += 32) {
                             uint32_t o[32];
                             tmem_ld32(tmem + kTmemO + c + lane_base, o);
                             tmem_wait_ld();
@@ -558,11 +587,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float ea = m_a == -INFINITY ? 0.f : m_a, eb = m_b == -INFINITY ? 0.f : m_b;
-                uint32_t pa[8], pb[8];
+                uint32_t pa[4], pb[4];
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const float a0 = ex2(__uint_as_float(r[4 * g]) - ea), a1 = ex2(__uint_as_float(r[4 * g + 1]) - ea);
-                    const float b0 = ex2(__uint_as_float(r[4 * g + 2]) - eb), b1 = ex2(__uint_as_float(r[4 * g + 3]) - eb);
+                for (int g = 0; g < 4; ++g) {
+                    const float a0 = ex2(fmaf(__uint_as_float(r[4 * g]), a.scale_log2, -ea));
+                    const float a1 = ex2(fmaf(__uint_as_float(r[4 * g + 1]), a.scale_log2, -ea));
+                    const float b0 = ex2(fmaf(__uint_as_float(r[4 * g + 2]), a.scale_log2, -eb));
+                    const float b1 = ex2(fmaf(__uint_as_float(r[4 * g + 3]), a.scale_log2, -eb));
                     l_a += a0 + a1;
                     l_b += b0 + b1;
                     // the weights enter the second product in the tensors' 16-bit type:
@@ -572,9 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (tile > 0) hold(&sh.pv_done, (tile - 1) & 1, ERR_WAIT_PART_FULL);
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    st_shared_u32(sbase + kOffP + ra * 128 + ((g ^ (ra & 7)) << 4) + c0 * 2, pa[g]);
-                    st_shared_u32(sbase + kOffP + rb * 128 + ((g ^ (rb & 7)) << 4) + c0 * 2, pb[g]);
+                for (int g = 0; g < 4; ++g) {
+                    const int u = half * 4 + g;
+                    st_shared_u32(sbase + kOffP + ra * 128 + ((u ^ (ra & 7)) << 4) + c0 * 2, pa[g]);
+                    st_shared_u32(sbase + kOffP + rb * 128 + ((u ^ (rb & 7)) << 4) + c0 * 2, pb[g]);
                 }
                 // rows past the last key hold whatever the page held: their weights are
                 // zero, but zero times a NaN is not
@@ -598,21 +630,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l_b += __shfl_xor_sync(0xffffffffu, l_b, o);
             }
             const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
-            named_bar_sync(1, kSoftThreads);   // factor and row_off are free again
+            if ((lane & 3) == 0) sh.half_of[half][ra] = l_a, sh.half_of[half][rb] = l_b;
+            named_bar_sync(1, kSoftThreads);   // factor and row_off are free again, too
             if ((lane & 3) == 0) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = e ? rb : ra;
-                    const float l = e ? l_b : l_a, m = e ? m_b : m_a;
-                    const int t = (r0 + r) / a.H, h = r0 + r - t * a.H;
-                    if (whole) {
-                        sh.factor[r] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
-                        sh.row_off[r] = r < rows ? (w.s.row0 + t) * a.o_st + h * a.o_sh : -1;
-                        if (a.lse && r < rows)
-                            a.lse[static_cast<int64_t>(w.s.row0 + t) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-                    } else if (r < rows) {
-                        a.part_ml[static_cast<int64_t>(slot) * kRows + r] = make_float2(m, l);
-                    }
+                // the two warps of 16 rows take eight each
+                const int r = half ? rb : ra;
+                const float l = sh.half_of[0][r] + sh.half_of[1][r], m = half ? m_b : m_a;
+                const int t = (r0 + r) / a.H, h = r0 + r - t * a.H;
+                if (whole) {
+                    sh.factor[r] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+                    sh.row_off[r] = r < rows ? (w.s.row0 + t) * a.o_st + h * a.o_sh : -1;
+                    if (a.lse && r < rows)
+                        a.lse[static_cast<int64_t>(w.s.row0 + t) * a.H + h] =
+                            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                } else if (r < rows) {
+                    a.part_ml[static_cast<int64_t>(slot) * kRows + r] = make_float2(m, l);
                 }
             }
             named_bar_sync(1, kSoftThreads);
@@ -621,55 +653,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             if (whole) {
-                // O^T (lanes: columns of the latent; columns: rows) leaves transposed, 32
-                // rows x 32 latent columns of a warp at a time, through the warp's own 2 KB
-                // of the weights' buffer: 16-byte stores, 64 bytes of a row per four lanes
-                const uint32_t stage = sbase + kOffP + warp * 2048;
+                // O^T (lanes: columns of the latent; columns: rows) leaves transposed, 16
+                // rows x 32 latent columns of a warp at a time, through the warp's 1 KB of
+                // the weights' buffer: 16-byte stores, 64 bytes of a row per four lanes.
+                // (The next weights are written behind the next tile's named barrier.)
+                const uint32_t stage = sbase + kOffP + warp * 1024;
                 const uint32_t st_row = lane & 7, st_chunk = lane >> 3;
-                T *out = static_cast<T *>(a.out) + warp * 32 + (lane & 3) * 8;
-                for (int c = 0; c < kGroups * kRows; c += 32) {
+                T *out = static_cast<T *>(a.out) + quad * 32 + (lane & 3) * 8;
+#pragma unroll
+                for (int c = 0; c < 2 * kRows; c += 32) {
                     uint32_t o0[16], o1[16];
                     if (n > 0) {
-                        tmem_ld_16x32(tmem + kTmemO + c + lane_base, o0);
-                        tmem_ld_16x32(tmem + kTmemO + c + lane_base + (16u << 16), o1);
+                        const uint32_t src = tmem + kTmemO + half * 2 * kRows + c + lane_base;
+                        tmem_ld_16x32(src, o0);
+                        tmem_ld_16x32(src + (16u << 16), o1);
                         tmem_wait_ld();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o0[i] = o1[i] = 0;
                     }
-                    const int rbase = c & 32;
-                    __syncwarp();   // the last 32 rows have been read
+                    T *dst = out + (half * 2 + c / kRows) * 128;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const float2 f = *reinterpret_cast<const float2 *>(&sh.factor[rbase + 8 * g + c0]);
-                        auto two = [&](const uint32_t *o) { return E::pack(__uint_as_float(o[0]) * f.x, __uint_as_float(o[1]) * f.y); };
-                        // rows of 64 bytes; the 16-byte unit is swizzled by the row pair
-                        stmatrix_x4_trans(stage + (8 * g + st_row) * 64 + ((st_chunk ^ (st_row >> 1)) << 4), two(o0 + 4 * g),
-                                          two(o0 + 4 * g + 2), two(o1 + 4 * g), two(o1 + 4 * g + 2));
-                    }
-                    __syncwarp();
-                    T *dst = out + (c / kRows) * 128;
+                    for (int g0 = 0; g0 < 4; g0 += 2) {
+                        const int rbase = (c & 32) + 8 * g0;
+                        __syncwarp();   // the last 16 rows have been read
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int r = 8 * g + (lane >> 2);
-                        const int64_t off = sh.row_off[rbase + r];
-                        const uint4 v = ld_shared_v4(stage + r * 64 + (((lane & 3) ^ ((r & 7) >> 1)) << 4));
-                        if (off >= 0) *reinterpret_cast<uint4 *>(dst + off) = v;
+                        for (int g = g0; g < g0 + 2; ++g) {
+                            const float2 f = *reinterpret_cast<const float2 *>(&sh.factor[(c & 32) + 8 * g + c0]);
+                            auto two = [&](const uint32_t *o) {
+                                return E::pack(__uint_as_float(o[0]) * f.x, __uint_as_float(o[1]) * f.y);
+                            };
+                            // rows of 64 bytes; the 16-byte unit is swizzled by the row pair
+                            stmatrix_x4_trans(stage + (8 * (g - g0) + st_row) * 64 + ((st_chunk ^ (st_row >> 1)) << 4),
+                                              two(o0 + 4 * g), two(o0 + 4 * g + 2), two(o1 + 4 * g), two(o1 + 4 * g + 2));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const int r = 8 * g + (lane >> 2);
+                            const int64_t off = sh.row_off[rbase + r];
+                            const uint4 v = ld_shared_v4(stage + r * 64 + (((lane & 3) ^ ((r & 7) >> 1)) << 4));
+                            if (off >= 0) *reinterpret_cast<uint4 *>(dst + off) = v;
+                        }
                     }
                 }
             } else {
-                float *part = a.part_o + static_cast<int64_t>(slot) * kRows * kMlaLatent + warp * 32 + lane;
-                for (int c = 0; c < kGroups * kRows; c += 32) {
+                float *part = a.part_o + static_cast<int64_t>(slot) * kRows * kMlaLatent + quad * 32 + lane;
+#pragma unroll
+                for (int c = 0; c < 2 * kRows; c += 32) {
                     uint32_t o[32];
                     if (n > 0) {
-                        tmem_ld32(tmem + kTmemO + c + lane_base, o);
+                        tmem_ld32(tmem + kTmemO + half * 2 * kRows + c + lane_base, o);
                         tmem_wait_ld();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0;
                     }
                     const int rbase = c & 32;
-                    float *dst = part + rbase * kMlaLatent + (c / kRows) * 128;
+                    float *dst = part + rbase * kMlaLatent + (half * 2 + c / kRows) * 128;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (rbase + i < rows) dst[i * kMlaLatent] = __uint_as_float(o[i]);
@@ -692,136 +733,184 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the partial results of the items that several CTAs shared: row by row
 //   M = max m_s,  O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s
 // over the item's parts in order. joins[c] = (the sequence's first query, first row of
-// the tile, rows, last CTA) of the item whose first part CTA c holds (rows 0: none). Four groups of 128
-// threads take every fourth part of a row, four columns each.
+// the tile, rows, last CTA) of the item whose first part CTA c holds (rows 0: none).
+// A large batch has two parts of each of 10,000 rows, a single long sequence 60 parts
+// of 64: a warp takes a whole row of up to kAhead parts; rows of more parts are shared
+// by a CTA, four warps per 128 columns.
 constexpr int kJoinThreads = 512;
 constexpr int kMaxCtas = 256;
+constexpr int kAhead = 8;    // parts whose sums are on their way together
+
+// Sum of parts [s0, s1) of a row for four columns, relative to their largest reference
+// maximum M, and the sum L of their exponentials (s1 - s0 <= 64).
+template <typename SlotOf>
+__device__ __forceinline__ float4 join_parts(const PagedArgs &a, SlotOf slot_of, int s0, int s1, int col, float &M, float &L) {
+    const int lane = threadIdx.x & 31;
+    float4 v[kAhead];
+    // the first sums are on their way while the weights are formed
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (s0 + k < s1) v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot_of(s0 + k) * kMlaLatent + col));
+    const float2 none = make_float2(-INFINITY, 0.f);
+    const float2 m0 = s0 + lane < s1 ? a.part_ml[slot_of(s0 + lane)] : none;
+    const float2 m1 = s0 + 32 + lane < s1 ? a.part_ml[slot_of(s0 + 32 + lane)] : none;
+    M = fmaxf(m0.x, m1.x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    // a part without visible keys has weight zero and sums of zero
+    const float w0 = m0.x == -INFINITY ? 0.f : ex2(m0.x - M), w1 = m1.x == -INFINITY ? 0.f : ex2(m1.x - M);
+    L = w0 * m0.y + w1 * m1.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < s1 - s0; k0 += kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (s0 + k0 + k < s1) {
+                const float f = __shfl_sync(0xffffffffu, k0 < 32 ? w0 : w1, (k0 + k) & 31);
+                acc.x += f * v[k].x, acc.y += f * v[k].y, acc.z += f * v[k].z, acc.w += f * v[k].w;
+                if (s0 + k0 + kAhead + k < s1)
+                    v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot_of(s0 + k0 + kAhead + k) * kMlaLatent + col));
+            }
+        }
+    }
+    return acc;
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs a, int ctas) {
-    __shared__ int s_rows[kMaxCtas + 1];   // rows of the joins before join c
-    __shared__ int s_sum[kMaxCtas / 32];
-    __shared__ float s_w[kMaxCtas];
-    __shared__ float s_l;
-    __shared__ float4 s_acc[3][128];
+__global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const PagedArgs a, int ctas) {
+    // rows before join c, of the joins of few parts and of many
+    __shared__ int s_rows[2][kMaxCtas + 1];
+    __shared__ int s_sum[2][kMaxCtas / 32];
+    __shared__ float4 s_acc[3][4][32];
+    __shared__ float2 s_ml[4];
     pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = warp & 3, grp = warp >> 2;
     pdl_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int4 mine = tid < ctas ? a.joins[tid] : make_int4(0, 0, 0, 0);
-    int inc = mine.z;
+    int rows = 0, inc = 0;
+    static_assert(kJoinThreads == 2 * kMaxCtas, "thread = (kind, join)");
+    {
+        const int c = tid % kMaxCtas;
+        const int4 j = c < ctas ? a.joins[c] : make_int4(0, 0, 0, 0);
+        const bool many = j.w - c + 1 > kAhead;
+        rows = many == (tid >= kMaxCtas) ? j.z : 0;
+        inc = rows;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
-    }
-    if (lane == 31 && warp < kMaxCtas / 32) s_sum[warp] = inc;
-    __syncthreads();
-    if (tid < kMaxCtas) {
-        for (int i = 0; i < warp; ++i) inc += s_sum[i];
-        s_rows[tid + 1] = inc;
-        if (tid == 0) s_rows[0] = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (lane == 31) s_sum[tid / kMaxCtas][c / 32] = inc;
     }
     __syncthreads();
-    const int total = s_rows[kMaxCtas];
-    for (int i = blockIdx.x; i < total; i += gridDim.x) {
-        int lo = 0, hi = kMaxCtas;   // the join with s_rows[lo] <= i < s_rows[lo + 1]
+    {
+        const int kind = tid / kMaxCtas, c = tid % kMaxCtas;
+        for (int i = 0; i < c / 32; ++i) inc += s_sum[kind][i];
+        s_rows[kind][c + 1] = inc;
+        if (c == 0) s_rows[kind][0] = 0;
+    }
+    __syncthreads();
+    const int col = slice * 128 + lane * 4;
+    auto find = [&](int kind, int i) {   // the join with s_rows[c] <= i < s_rows[c + 1]
+        int lo = 0, hi = kMaxCtas;
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            (s_rows[mid] <= i ? lo : hi) = mid;
+            (s_rows[kind][mid] <= i ? lo : hi) = mid;
         }
-        const int c = lo, r = i - s_rows[c];
+        return lo;
+    };
+    auto store = [&](const int4 &j, int r, int col, float4 acc, float M, float L) {
+        const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);
+        const int t = (j.y + r) / a.H, h = j.y + r - t * a.H;
+        const int64_t q = j.x + t;
+        T *dst = static_cast<T *>(a.out) + q * a.o_st + h * a.o_sh + col;
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(Elem<T>::pack(acc.x * inv, acc.y * inv), Elem<T>::pack(acc.z * inv, acc.w * inv));
+        if (a.lse && col == 0) a.lse[q * a.H + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    };
+    for (int i = (kJoinThreads / 32) * blockIdx.x + warp; i < s_rows[0][kMaxCtas]; i += (kJoinThreads / 32) * gridDim.x) {
+        const int c = find(0, i), r = i - s_rows[0][c];
         const int4 j = a.joins[c];
         const int parts = j.w - c + 1;
         auto slot_of = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * kRows + r; };
-        const int grp = tid >> 7, col = tid & 127;
-        // the first sums are on their way while the weights are formed
-        constexpr int kAhead = 8;
-        float4 v[kAhead];
+        auto sums_of = [&](int s, int k) {
+            return __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot_of(s) * kMlaLatent + k * 128 + lane * 4));
+        };
+        float4 v[2][4];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int s = grp + 4 * k;
-            v[k] = s < parts ? *reinterpret_cast<const float4 *>(a.part_o + slot_of(s) * kMlaLatent + col * 4)
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        float M = -INFINITY;
-        if (warp == 0) {
-            float2 ml[kMaxCtas / 32];
-            float L = 0.f;
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int k = 0; k < kMaxCtas / 32; ++k) {
-                const int s = lane + 32 * k;
-                ml[k] = s < parts ? a.part_ml[slot_of(s)] : make_float2(-INFINITY, 0.f);
-                M = fmaxf(M, ml[k].x);
-            }
+            for (int k = 0; k < 4; ++k) v[s][k] = sums_of(s, k);
+        const float2 ml = lane < parts ? a.part_ml[slot_of(lane)] : make_float2(-INFINITY, 0.f);
+        float M = ml.x;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int o = kAhead / 2; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        M = __shfl_sync(0xffffffffu, M, 0);
+        // a part without visible keys has weight zero and sums of zero
+        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        float L = w * ml.y;
 #pragma unroll
-            for (int k = 0; k < kMaxCtas / 32; ++k) {
-                ml[k].x = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
-                L += ml[k].x * ml[k].y;
-            }
+        for (int o = kAhead / 2; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        L = __shfl_sync(0xffffffffu, L, 0);
+        float4 acc[4] = {};
+        for (int s0 = 0; s0 < parts; s0 += 2)
 #pragma unroll
-            for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);
+            for (int s = 0; s < 2; ++s) {
+                if (s0 + s >= parts) break;
+                const float f = __shfl_sync(0xffffffffu, w, s0 + s);
 #pragma unroll
-            for (int k = 0; k < kMaxCtas / 32; ++k)
-                if (lane + 32 * k < parts) s_w[lane + 32 * k] = ml[k].x * inv;
-            if (lane == 0) s_l = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-        }
-        __syncthreads();
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s0 = grp; s0 < parts; s0 += 4 * kAhead) {
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int s = s0 + 4 * k;
-                // a part without visible keys has weight zero and sums of zero
-                if (s < parts) {
-                    const float w = s_w[s];
-                    acc.x += w * v[k].x, acc.y += w * v[k].y, acc.z += w * v[k].z, acc.w += w * v[k].w;
+                for (int k = 0; k < 4; ++k) {
+                    acc[k].x += f * v[s][k].x, acc[k].y += f * v[s][k].y, acc[k].z += f * v[s][k].z, acc[k].w += f * v[s][k].w;
+                    if (s0 + s + 2 < parts) v[s][k] = sums_of(s0 + s + 2, k);
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int s = s0 + 4 * (kAhead + k);
-                if (s < parts) v[k] = *reinterpret_cast<const float4 *>(a.part_o + slot_of(s) * kMlaLatent + col * 4);
-            }
-        }
-        if (grp > 0) s_acc[grp - 1][col] = acc;
+        for (int k = 0; k < 4; ++k) store(j, r, k * 128 + lane * 4, acc[k], M, L);
+    }
+    for (int i = blockIdx.x; i < s_rows[1][kMaxCtas]; i += gridDim.x) {
+        const int c = find(1, i), r = i - s_rows[1][c];
+        const int4 j = a.joins[c];
+        const int parts = j.w - c + 1, per = (parts + 3) / 4;
+        auto slot_of = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * kRows + r; };
+        float M, L;
+        float4 acc = join_parts(a, slot_of, min(parts, grp * per), min(parts, (grp + 1) * per), col, M, L);
+        __syncthreads();   // the last row's sums have been read
+        if (grp > 0) s_acc[grp - 1][slice][lane] = acc;
+        if (slice == 0 && lane == 0) s_ml[grp] = make_float2(M, L);
         __syncthreads();
         if (grp == 0) {
+            float m = M;
 #pragma unroll
-            for (int g = 0; g < 3; ++g) {
-                const float4 x = s_acc[g][col];
-                acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+            for (int g = 1; g < 4; ++g) m = fmaxf(m, s_ml[g].x);
+            float f = M == -INFINITY ? 0.f : ex2(M - m);
+            L *= f;
+            acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+            for (int g = 1; g < 4; ++g) {
+                f = s_ml[g].x == -INFINITY ? 0.f : ex2(s_ml[g].x - m);
+                L += f * s_ml[g].y;
+                const float4 x = s_acc[g - 1][slice][lane];
+                acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
             }
-            const int t = (j.y + r) / a.H, h = j.y + r - t * a.H;
-            const int64_t q = j.x + t;
-            T *dst = static_cast<T *>(a.out) + q * a.o_st + h * a.o_sh + col * 4;
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(Elem<T>::pack(acc.x, acc.y), Elem<T>::pack(acc.z, acc.w));
-            if (a.lse && tid == 0) a.lse[q * a.H + h] = s_l;
+            store(j, r, col, acc, m, L);
         }
-        __syncthreads();   // s_w, s_l and s_acc are reused by the next row
     }
 }
 
 template <typename T>
-cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &lat, const CUtensorMap &rope, const PagedArgs &a, int grid,
-                     cudaStream_t stream) {
+cudaError_t launch_t(const PagedMaps &m, const PagedArgs &a, int grid, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(paged_attn_kernel<T>, kSmem, done);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(paged_attn_kernel<T>, dim3(grid), dim3(kThreads), kSmem, stream, q, lat, rope, a);
+    e = launch_pdl(paged_attn_kernel<T>, dim3(grid), dim3(kThreads), kSmem, stream, m, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(paged_join_kernel<T>, dim3(2 * grid), dim3(kJoinThreads), 0, stream, a, grid);
 }
 
 }  // namespace
 
-cudaError_t launch_paged(const CUtensorMap &q, const CUtensorMap &latent, const CUtensorMap &rope, const PagedArgs &a,
-                         bool bf16, int grid, cudaStream_t stream) {
+cudaError_t launch_paged(const PagedMaps &m, const PagedArgs &a, bool bf16, int grid, cudaStream_t stream) {
     if (grid > kMaxCtas) return cudaErrorInvalidValue;
-    return bf16 ? launch_t<__nv_bfloat16>(q, latent, rope, a, grid, stream)
-                : launch_t<__half>(q, latent, rope, a, grid, stream);
+    return bf16 ? launch_t<__nv_bfloat16>(m, a, grid, stream) : launch_t<__half>(m, a, grid, stream);
 }
 
 }  // namespace moe
