@@ -735,10 +735,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // over the item's parts in order. joins[c] = (the sequence's first query, first row of
 // the tile, rows, last CTA) of the item whose first part CTA c holds (rows 0: none).
 // A large batch has two parts of each of 10,000 rows, a single long sequence 60 parts
-// of 64: a warp takes a whole row of up to kAhead parts; rows of more parts are shared
-// by a CTA, four warps per 128 columns.
+// of 64: a warp takes a whole row of up to kAhead parts; rows of more are shared by a
+// CTA, four warps per 128 columns, unless there are enough rows to fill the GPU with
+// a warp each (up to 32 parts: 33 rows' worth of 64 with 6 to 10 parts, 14 -> 9 us).
 constexpr int kJoinThreads = 512;
 constexpr int kMaxCtas = 256;
+constexpr int kFewJoins = 8;
 constexpr int kAhead = 8;    // parts whose sums are on their way together
 
 // Sum of parts [s0, s1) of a row for four columns, relative to their largest reference
@@ -792,7 +794,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
     {
         const int c = tid % kMaxCtas;
         const int4 j = c < ctas ? a.joins[c] : make_int4(0, 0, 0, 0);
-        const bool many = j.w - c + 1 > kAhead;
+        const int joins = __syncthreads_count(tid < kMaxCtas && j.z > 0);
+        const bool many = j.w - c + 1 > (joins > kFewJoins ? 32 : kAhead);
         rows = many == (tid >= kMaxCtas) ? j.z : 0;
         inc = rows;
 #pragma unroll
@@ -843,13 +846,13 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
         const float2 ml = lane < parts ? a.part_ml[slot_of(lane)] : make_float2(-INFINITY, 0.f);
         float M = ml.x;
 #pragma unroll
-        for (int o = kAhead / 2; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         M = __shfl_sync(0xffffffffu, M, 0);
         // a part without visible keys has weight zero and sums of zero
         const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
         float L = w * ml.y;
 #pragma unroll
-        for (int o = kAhead / 2; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         L = __shfl_sync(0xffffffffu, L, 0);
         float4 acc[4] = {};
         for (int s0 = 0; s0 < parts; s0 += 2)
