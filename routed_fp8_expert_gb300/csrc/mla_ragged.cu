@@ -29,13 +29,13 @@ constexpr int kPerTile = 5;                      // 3 pieces of K, 2 of V
 constexpr int kOffRing = 2 * kQPieces * kPiece;
 constexpr int kOffMisc = kOffRing + kSlots * kPiece;
 constexpr int kSmem = kOffMisc + 1024;
-constexpr int kThreads = 2 * kTile + 64;         // a warpgroup per row tile, loads, MMA
+constexpr int kThreads = 3 * kTile;              // a warpgroup per row tile; loads and MMA (two warps idle)
 constexpr float kLag = 8.0f;                     // see mla_paged.cu
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 struct Shared {
     uint64_t full[kSlots], empty[kSlots];
-    uint64_t q_full, s_full[2], p_full[2], o_full[2], mma_done;
+    uint64_t q_full, s_full[2], p_full[2][2], o_full[2], mma_done;
     uint32_t tmem;
     int abort;
 };
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh.q_full), 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&sh.s_full[t]), 1);
-            mbar_init(smem_u32(&sh.p_full[t]), kTile);
+            mbar_init(smem_u32(&sh.p_full[t][0]), kTile), mbar_init(smem_u32(&sh.p_full[t][1]), kTile);
             mbar_init(smem_u32(&sh.o_full[t]), 1);
         }
         mbar_init(smem_u32(&sh.mma_done), 1);
@@ -95,6 +95,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sh.tmem;
     const Waiter wait{smem_u32(&sh.abort), a.err};
 
+    // 384 threads x 168 registers are the launch's; the third warpgroup gives 80 of its
+    // 168 to the other two, which hold a row's 128 scores (2 x 208 + 88 = 3 x 168). The
+    // instructions stand inside the branches: the compiler takes each as the budget of
+    // what it dominates.
+    if (warp >= 8) regs_down<88>();
     if (warp == 8) {
         // -------------------------------------------------------- loads
         if (lane == 0 && tiles > 0) {
@@ -162,12 +167,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < nt && ok; ++t) {
                     // the values first: the warpgroup of row tile 0 clears rows past the end
                     if (t == 0 && !(arrived(v0) && arrived(v0 + 1))) { ok = false; break; }
-                    if (!wait(smem_u32(&sh.p_full[t]), j & 1, ERR_WAIT_PART_FULL)) { ok = false; break; }
-                    tc_fence_after();
                     const uint32_t p = tmem + t * kTile, o = tmem + 2 * kTile + t * kMlaV;
                     const uint32_t b0 = sbase + kOffRing + s0 * kPiece, b1 = sbase + kOffRing + s1 * kPiece;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
+                        if (k % 4 == 0) {
+                            if (!wait(smem_u32(&sh.p_full[t][k / 4]), j & 1, ERR_WAIT_PART_FULL)) { ok = false; break; }
+                            tc_fence_after();
+                        }
                         const uint32_t acc = j > 0 || k > 0;
                         if (s1 == s0 + 1) {
                             mma_16_ts(o, p + k * 8, sdesc_mn_sw128(b0 + k * 2048, kPiece), id_o, acc);
@@ -176,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_16_ts(o + 64, p + k * 8, sdesc_mn_sw128(b1 + k * 2048, kPiece), id_o64, acc);
                         }
                     }
+                    if (!ok) break;
                     if (t == nt - 1) {
                         mma_commit(smem_u32(&sh.empty[s0]));
                         mma_commit(smem_u32(&sh.empty[s1]));
@@ -190,8 +198,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_drain(smem_u32(&sh.mma_done), 0, a.err);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 8) {
         // -------------------------------------------------------- softmax and results
+        regs_up<208>();
         const int t = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + t * kTile + lanes, to = tmem + 2 * kTile + t * kMlaV + lanes;
@@ -222,12 +231,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 32; ++i)
                             if (kb + c * 32 + i >= vis) r[c][i] = __float_as_uint(-INFINITY);
                 }
-                float mx = -INFINITY;
+                if (t == 0 && nk - kb < kTile) {
+                    // value rows past the sequence's end: their weights are zero, but
+                    // zero times a NaN is not. The rows are the next sequence's.
+                    const uint32_t v0 = j * kPerTile + 3;
+                    for (int c = 0; c < 2; ++c)
+                        hold(&sh.full[(v0 + c) % kSlots], ((v0 + c) / kSlots) & 1, ERR_WAIT_TMA_FULL);
+                    const int left = nk - kb, per = (kTile - left) * 8;
+                    for (int i = threadIdx.x; i < 2 * per; i += kTile) {
+                        const int c = i >= per;
+                        st_shared_v4(sbase + kOffRing + ((v0 + c) % kSlots) * kPiece + left * 128 + (i - c * per) * 16,
+                                     make_uint4(0, 0, 0, 0));
+                    }
+                    fence_async_smem();
+                }
+                float top[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    top[c] = __uint_as_float(r[c][0]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[c][i]));
-                mx *= a.scale_log2;
+                    for (int i = 1; i < 31; i += 2)
+                        top[c] = fmaxf(top[c], fmaxf(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])));
+                    top[c] = fmaxf(top[c], __uint_as_float(r[c][31]));
+                }
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
                 const bool behind = mx > m + kLag;
                 if (__any_sync(0xffffffffu, behind)) {
                     const float mn = fmaxf(m, mx);
@@ -249,37 +276,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float e = m == -INFINITY ? 0.f : m;
-                uint32_t p[2][32];
+                const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), neg2 = pack_f32x2(-e, -e);
+                uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int hh = 0; hh < 2; ++hh) {
+                    // 64 keys: the product starts on them while the rest is computed
+                    uint32_t p[32];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float p0 = ex2(fmaf(__uint_as_float(r[c][i]), a.scale_log2, -e));
-                        const float p1 = ex2(fmaf(__uint_as_float(r[c][i + 1]), a.scale_log2, -e));
-                        l += p0 + p1;
-                        // the weights enter the second product in the tensors' 16-bit
-                        // type: half an ulp each, averaged over the keys
-                        p[c >> 1][(c & 1) * 16 + i / 2] = E::pack(p0, p1);
-                    }
-                    if (c & 1) tmem_st32(ts + (c >> 1) * 32, p[c >> 1]);
-                }
-                if (t == 0 && nk - kb < kTile) {
-                    // value rows past the sequence's end: their weights are zero, but
-                    // zero times a NaN is not. The rows are the next sequence's.
-                    const uint32_t v0 = j * kPerTile + 3;
                     for (int c = 0; c < 2; ++c)
-                        hold(&sh.full[(v0 + c) % kSlots], ((v0 + c) / kSlots) & 1, ERR_WAIT_TMA_FULL);
-                    const int left = nk - kb, per = (kTile - left) * 8;
-                    for (int i = threadIdx.x; i < 2 * per; i += kTile) {
-                        const int c = i >= per;
-                        st_shared_v4(sbase + kOffRing + ((v0 + c) % kSlots) * kPiece + left * 128 + (i - c * per) * 16,
-                                     make_uint4(0, 0, 0, 0));
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const uint64_t s2 = pack_f32x2(__uint_as_float(r[2 * hh + c][i]), __uint_as_float(r[2 * hh + c][i + 1]));
+                            const float2 x = unpack_f32x2(fma_f32x2(s2, scale2, neg2));
+                            const float p0 = ex2(x.x), p1 = ex2(x.y);
+                            sum[(i / 2) & 3] = add_f32x2(sum[(i / 2) & 3], pack_f32x2(p0, p1));
+                            // the weights enter the second product in the tensors' 16-bit
+                            // type: half an ulp each, averaged over the keys
+                            p[c * 16 + i / 2] = E::pack(p0, p1);
+                        }
+                    tmem_st32(ts + hh * 32, p);
+                    if (hh == 0) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(smem_u32(&sh.p_full[t][0]));
                     }
-                    fence_async_smem();
                 }
+                const float2 both = unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])));
+                l += both.x + both.y;
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(smem_u32(&sh.p_full[t]));
+                mbar_arrive(smem_u32(&sh.p_full[t][1]));
             }
             if (tiles > 0) {
                 hold(&sh.o_full[t], 0, ERR_WAIT_PART_FULL);
