@@ -227,6 +227,20 @@ struct Waiter {
     }
 };
 
+// The same for issuing loops: the path that has to wait stays out of line, so that many
+// waits leave the loop small enough for the instruction cache.
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort_addr, unsigned int *err,
+                                              uint32_t bit) {
+    return mbar_wait(bar, parity, abort_addr, err, bit);
+}
+struct IssueWaiter {
+    uint32_t abort_addr;
+    unsigned int *err;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, uint32_t bit) const {
+        return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_addr, err, bit);
+    }
+};
+
 // ---------------------------------------------------------------- argument blocks
 
 struct RopeArgs {

@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 9) {
         // -------------------------------------------------------- MMA issue
         if (tiles > 0 && elect_one()) {
+            const IssueWaiter wait{smem_u32(&sh.abort), a.err};
             constexpr uint32_t id_s = idesc16(E::kFmt, kTile, kTile);
             constexpr uint32_t id_o = idesc16(E::kFmt, kTile, kMlaV, false, true);
             constexpr uint32_t id_o64 = idesc16(E::kFmt, kTile, 64, false, true);
@@ -143,44 +144,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto arrived = [&](uint32_t piece) {
                 return wait(smem_u32(&sh.full[slot_of(piece)]), (piece / kSlots) & 1, ERR_WAIT_TMA_FULL);
             };
-            // S_t of key tile j; the last row tile frees the pieces of K
-            auto scores = [&](int j, int t) -> bool {
-                for (int c = 0; c < 3; ++c) {
-                    const uint32_t piece = j * kPerTile + c;
-                    if (t == 0 && !arrived(piece)) return false;
-                    tc_fence_after();
-                    const uint32_t kb = sbase + kOffRing + slot_of(piece) * kPiece;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_16_ss(tmem + t * kTile, sdesc_sw128(sbase + (t * kQPieces + c) * kPiece + k * 32),
-                                 sdesc_sw128(kb + k * 32), id_s, c > 0 || k > 0);
-                    if (t == nt - 1) mma_commit(smem_u32(&sh.empty[slot_of(piece)]));
-                }
-                mma_commit(smem_u32(&sh.s_full[t]));
-                return true;
-            };
+            const uint64_t dq = sdesc_sw128(sbase), dk = sdesc_sw128(sbase + kOffRing);
+            const uint64_t dv = sdesc_mn_sw128(sbase + kOffRing, kPiece);
+            // One loop body issues a row tile's product with V and then its next scores; row
+            // tiles take turns. The body stays small on purpose: unrolled over the row
+            // tiles it outgrew the instruction cache beside the softmax's code, and every
+            // turn of the loop cost 900 cycles.
             bool ok = wait(smem_u32(&sh.q_full), 0, ERR_WAIT_TMA_FULL);
-            for (int t = 0; t < nt && ok; ++t) ok = scores(0, t);
-            for (int j = 0; j < tiles && ok; ++j) {
-                const uint32_t v0 = j * kPerTile + 3;
-                const uint32_t s0 = slot_of(v0), s1 = slot_of(v0 + 1);
-                for (int t = 0; t < nt && ok; ++t) {
-                    // the values first: the warpgroup of row tile 0 clears rows past the end
-                    if (t == 0 && !(arrived(v0) && arrived(v0 + 1))) { ok = false; break; }
+            const int steps = tiles * nt;
+#pragma unroll 1
+            for (int i = -nt; i < steps && ok; ++i) {
+                const int t = two ? i & 1 : 0, j = two ? i >> 1 : i;   // -1: the first scores
+                if (j >= 0) {
+                    const uint32_t v0 = j * kPerTile + 3, s0 = slot_of(v0), s1 = slot_of(v0 + 1);
+                    if (t == 0 && !(arrived(v0) && arrived(v0 + 1))) break;
                     const uint32_t p = tmem + t * kTile, o = tmem + 2 * kTile + t * kMlaV;
-                    const uint32_t b0 = sbase + kOffRing + s0 * kPiece, b1 = sbase + kOffRing + s1 * kPiece;
+                    const uint64_t b0 = dv + (s0 * kPiece >> 4);
+                    const uint32_t acc0 = j > 0;
+                    if (!wait(smem_u32(&sh.p_full[t][0]), j & 1, ERR_WAIT_PART_FULL)) break;
+                    tc_fence_after();
+                    if (s1 == s0 + 1) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (k % 4 == 0) {
-                            if (!wait(smem_u32(&sh.p_full[t][k / 4]), j & 1, ERR_WAIT_PART_FULL)) { ok = false; break; }
-                            tc_fence_after();
+                        for (int k = 0; k < 8; ++k) {
+                            if (k == 4) {
+                                if (!wait(smem_u32(&sh.p_full[t][1]), j & 1, ERR_WAIT_PART_FULL)) { ok = false; break; }
+                                tc_fence_after();
+                            }
+                            mma_16_ts(o, p + k * 8, b0 + (k * 2048 >> 4), id_o, k > 0 ? 1 : acc0);
                         }
-                        const uint32_t acc = j > 0 || k > 0;
-                        if (s1 == s0 + 1) {
-                            mma_16_ts(o, p + k * 8, sdesc_mn_sw128(b0 + k * 2048, kPiece), id_o, acc);
-                        } else {   // the two pieces lie at the ring's end and start
-                            mma_16_ts(o, p + k * 8, sdesc_mn_sw128(b0 + k * 2048, kPiece), id_o64, acc);
-                            mma_16_ts(o + 64, p + k * 8, sdesc_mn_sw128(b1 + k * 2048, kPiece), id_o64, acc);
+                    } else {   // the two pieces lie at the ring's end and start
+                        const uint64_t b1 = dv + (s1 * kPiece >> 4);
+                        ok = wait(smem_u32(&sh.p_full[t][1]), j & 1, ERR_WAIT_PART_FULL);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < 8 && ok; ++k) {
+                            mma_16_ts(o, p + k * 8, b0 + (k * 2048 >> 4), id_o64, k > 0 ? 1 : acc0);
+                            mma_16_ts(o + 64, p + k * 8, b1 + (k * 2048 >> 4), id_o64, k > 0 ? 1 : acc0);
                         }
                     }
                     if (!ok) break;
@@ -189,9 +188,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_commit(smem_u32(&sh.empty[s1]));
                     }
                     if (j == tiles - 1) mma_commit(smem_u32(&sh.o_full[t]));
-                    // MMAs run in issue order: S_t of the next tile overwrites P_t after
-                    // the product above has read it
-                    if (j + 1 < tiles) ok = scores(j + 1, t);
+                }
+                if (j + 1 < tiles) {
+                    // S_t of the next tile. MMAs run in issue order: it overwrites P_t
+                    // after the product above has read it. The last row tile frees K.
+                    const uint64_t q = dq + (t * kQPieces * kPiece >> 4);
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        const uint32_t piece = (j + 1) * kPerTile + c, slot = slot_of(piece);
+                        if (t == 0) {
+                            if (!arrived(piece)) { ok = false; break; }
+                            tc_fence_after();
+                        }
+                        const uint64_t kd = dk + (slot * kPiece >> 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_16_ss(tmem + t * kTile, q + (c * kPiece + k * 32 >> 4), kd + (k * 32 >> 4), id_s, c > 0 || k > 0);
+                        if (t == nt - 1) mma_commit(smem_u32(&sh.empty[slot]));
+                    }
+                    if (ok) mma_commit(smem_u32(&sh.s_full[t]));
                 }
             }
             mma_commit(smem_u32(&sh.mma_done));
