@@ -218,6 +218,31 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Work stealing: asks for a CTA of this launch that has not started yet, to run its work
+// here instead. The 16-byte answer counts on `bar` like a copy. After an answer
+// without a CTA no further request may be made.
+__device__ __forceinline__ void clc_request(uint32_t answer, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+        "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ bool clc_answer(uint32_t answer, int &x, int &y, int &z) {
+    uint32_t ok, cx, cy, cz;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%4];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, h;\n\t}"
+        : "=r"(ok), "=r"(cx), "=r"(cy), "=r"(cz)
+        : "r"(answer)
+        : "memory");
+    x = cx, y = cy, z = cz;
+    return ok != 0;
+}
+
 // Bounded wait of a whole role: false once any role of the CTA has given up.
 struct Waiter {
     uint32_t abort_addr;

@@ -34,7 +34,7 @@ constexpr float kLag = 8.0f;                     // see mla_paged.cu
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 struct Shared {
-    uint64_t full[kSlots], empty[kSlots];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];   // of every other key tile
     uint64_t q_full, s_full[2], p_full[2][2], o_full[2], mma_done;
     uint32_t tmem;
     int abort;
@@ -77,9 +77,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tiles = (keys + kTile - 1) / kTile;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(&sh.full[i]), 1), mbar_init(smem_u32(&sh.empty[i]), 1);
         mbar_init(smem_u32(&sh.q_full), 1);
         for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&sh.k_full[t]), 1), mbar_init(smem_u32(&sh.k_empty[t]), 1);
+            mbar_init(smem_u32(&sh.v_full[t]), 1), mbar_init(smem_u32(&sh.v_empty[t]), 1);
             mbar_init(smem_u32(&sh.s_full[t]), 1);
             mbar_init(smem_u32(&sh.p_full[t][0]), kTile), mbar_init(smem_u32(&sh.p_full[t][1]), kTile);
             mbar_init(smem_u32(&sh.o_full[t]), 1);
@@ -92,7 +93,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    // all 512 columns are this CTA's, so its tensor memory starts at address 0: a
+    // constant costs the MMA issue nothing
+    constexpr uint32_t tmem = 0;
     const Waiter wait{smem_u32(&sh.abort), a.err};
 
     // 384 threads x 168 registers are the launch's; the third warpgroup gives 80 of its
@@ -109,27 +112,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < kQPieces; ++c)
                     tma_load_3d(sbase + (t * kQPieces + c) * kPiece, &map_q, smem_u32(&sh.q_full), c * 64, h,
                                 static_cast<int>(q0) + r0 + t * kTile, pol);
-            uint32_t piece = 0, used = 0, parity = 0;
-            bool ok = true;
-            for (int j = 0; j < tiles && ok; ++j) {
-                const int key = static_cast<int>(kk0) + j * kTile;
-                for (int c = 0; c < kPerTile; ++c, ++piece) {
-                    const int slot = piece % kSlots;
-                    const uint32_t ph = (piece / kSlots) & 1;
-                    if (!wait(smem_u32(&sh.empty[slot]), ph ^ 1, ERR_WAIT_SMEM_EMPTY)) { ok = false; break; }
-                    const uint32_t full = smem_u32(&sh.full[slot]), dst = sbase + kOffRing + slot * kPiece;
-                    mbar_arrive_expect_tx(full, kPiece);
-                    if (c < 2) tma_load_3d(dst, &map_kn, full, c * 64, h, key, pol);
-                    else if (c == 2) tma_load_2d(dst, &map_kp, full, 0, key, pol);
-                    else tma_load_3d(dst, &map_v, full, (c - 3) * 64, h, key, pol);
-                    used |= 1u << slot;
-                    parity = (parity & ~(1u << slot)) | (ph << slot);
-                }
+            int g = 0;
+            for (; g < tiles; ++g) {
+                const int key = static_cast<int>(kk0) + g * kTile;
+                // The pieces take the slots of those eight before them: the third of K and
+                // the two of V of two tiles ago, and the first two of the last K.
+                const uint32_t two_ago = ((g >> 1) & 1) ^ 1, one_ago = ((g - 1) >> 1) & 1;
+                const uint32_t kf = smem_u32(&sh.k_full[g & 1]), vf = smem_u32(&sh.v_full[g & 1]);
+                auto dst = [&](int c) { return sbase + kOffRing + ((g * kPerTile + c) % kSlots) * kPiece; };
+                if (!wait(smem_u32(&sh.k_empty[g & 1]), two_ago, ERR_WAIT_SMEM_EMPTY)) break;
+                mbar_arrive_expect_tx(kf, 3 * kPiece);
+                tma_load_3d(dst(0), &map_kn, kf, 0, h, key, pol);
+                if (!wait(smem_u32(&sh.v_empty[g & 1]), two_ago, ERR_WAIT_SMEM_EMPTY)) break;
+                tma_load_3d(dst(1), &map_kn, kf, 64, h, key, pol);
+                tma_load_2d(dst(2), &map_kp, kf, 0, key, pol);
+                if (g > 0 && !wait(smem_u32(&sh.k_empty[(g - 1) & 1]), one_ago, ERR_WAIT_SMEM_EMPTY)) break;
+                mbar_arrive_expect_tx(vf, 2 * kPiece);
+                tma_load_3d(dst(3), &map_v, vf, 0, h, key, pol);
+                tma_load_3d(dst(4), &map_v, vf, 64, h, key, pol);
             }
             // the last loads must land before the CTA may exit
             mbar_wait_drain(smem_u32(&sh.q_full), 0, a.err);
-            for (int i = 0; i < kSlots; ++i)
-                if (used >> i & 1) mbar_wait_drain(smem_u32(&sh.full[i]), parity >> i & 1, a.err);
+            for (int i = g < 2 ? 0 : g - 2; i < g; ++i) {
+                mbar_wait_drain(smem_u32(&sh.k_full[i & 1]), (i >> 1) & 1, a.err);
+                mbar_wait_drain(smem_u32(&sh.v_full[i & 1]), (i >> 1) & 1, a.err);
+            }
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -140,28 +147,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t id_o = idesc16(E::kFmt, kTile, kMlaV, false, true);
             constexpr uint32_t id_o64 = idesc16(E::kFmt, kTile, 64, false, true);
             const int nt = two ? 2 : 1;
-            auto slot_of = [](uint32_t piece) { return piece % kSlots; };
-            auto arrived = [&](uint32_t piece) {
-                return wait(smem_u32(&sh.full[slot_of(piece)]), (piece / kSlots) & 1, ERR_WAIT_TMA_FULL);
-            };
             const uint64_t dq = sdesc_sw128(sbase), dk = sdesc_sw128(sbase + kOffRing);
             const uint64_t dv = sdesc_mn_sw128(sbase + kOffRing, kPiece);
+            // A third of S_t of key tile g. MMAs run in issue order: S_t overwrites P_t after
+            // the product before has read it.
+            auto scores = [&](int t, uint32_t g, int c) {
+                const uint64_t q = dq + ((t * kQPieces + c) * kPiece >> 4);
+                const uint64_t kd = dk + (((g * kPerTile + c) % kSlots) * kPiece >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_16_ss(tmem + t * kTile, q + (k * 32 >> 4), kd + (k * 32 >> 4), id_s, c > 0 || k > 0);
+            };
+            auto k_test = [&](uint32_t g) { return mbar_test(smem_u32(&sh.k_full[g & 1]), (g >> 1) & 1); };
+            auto k_wait = [&](uint32_t g) { return wait(smem_u32(&sh.k_full[g & 1]), (g >> 1) & 1, ERR_WAIT_TMA_FULL); };
+            auto v_test = [&](uint32_t g) { return mbar_test(smem_u32(&sh.v_full[g & 1]), (g >> 1) & 1); };
+            auto v_wait = [&](uint32_t g) { return wait(smem_u32(&sh.v_full[g & 1]), (g >> 1) & 1, ERR_WAIT_TMA_FULL); };
             // One loop body issues a row tile's product with V and then its next scores; row
-            // tiles take turns. The body stays small on purpose: unrolled over the row
-            // tiles it outgrew the instruction cache beside the softmax's code, and every
-            // turn of the loop cost 900 cycles.
-            bool ok = wait(smem_u32(&sh.q_full), 0, ERR_WAIT_TMA_FULL);
+            // tiles take turns, one at its exponentials while the other multiplies. The body
+            // stays small on purpose: unrolled over the row tiles it outgrew the instruction
+            // cache beside the softmax's code, and every turn of the loop cost 900 cycles.
+            // A barrier test takes about 100 cycles and few MMAs are queued: the tests for
+            // the next step are made between the present one's MMAs.
+            bool ok = wait(smem_u32(&sh.q_full), 0, ERR_WAIT_TMA_FULL), ready = false;
             const int steps = tiles * nt;
 #pragma unroll 1
             for (int i = -nt; i < steps && ok; ++i) {
-                const int t = two ? i & 1 : 0, j = two ? i >> 1 : i;   // -1: the first scores
+                const int t = two ? i & 1 : 0, j = two ? i >> 1 : i;   // j = -1: the first scores
+                const bool last_t = t == nt - 1;
                 if (j >= 0) {
-                    const uint32_t v0 = j * kPerTile + 3, s0 = slot_of(v0), s1 = slot_of(v0 + 1);
-                    if (t == 0 && !(arrived(v0) && arrived(v0 + 1))) break;
+                    // the product's V and the first half of its weights
+                    if (!ready && !(v_wait(j) && wait(smem_u32(&sh.p_full[t][0]), j & 1, ERR_WAIT_PART_FULL))) break;
+                    const uint32_t s0 = (j * kPerTile + 3) % kSlots, s1 = (j * kPerTile + 4) % kSlots;
                     const uint32_t p = tmem + t * kTile, o = tmem + 2 * kTile + t * kMlaV;
                     const uint64_t b0 = dv + (s0 * kPiece >> 4);
                     const uint32_t acc0 = j > 0;
-                    if (!wait(smem_u32(&sh.p_full[t][0]), j & 1, ERR_WAIT_PART_FULL)) break;
                     tc_fence_after();
                     if (s1 == s0 + 1) {
 #pragma unroll
@@ -183,30 +202,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (!ok) break;
-                    if (t == nt - 1) {
-                        mma_commit(smem_u32(&sh.empty[s0]));
-                        mma_commit(smem_u32(&sh.empty[s1]));
-                    }
+                    if (last_t) mma_commit(smem_u32(&sh.v_empty[j & 1]));   // the last row tile frees V
                     if (j == tiles - 1) mma_commit(smem_u32(&sh.o_full[t]));
                 }
-                if (j + 1 < tiles) {
-                    // S_t of the next tile. MMAs run in issue order: it overwrites P_t
-                    // after the product above has read it. The last row tile frees K.
-                    const uint64_t q = dq + (t * kQPieces * kPiece >> 4);
-#pragma unroll
-                    for (int c = 0; c < 3; ++c) {
-                        const uint32_t piece = (j + 1) * kPerTile + c, slot = slot_of(piece);
-                        if (t == 0) {
-                            if (!arrived(piece)) { ok = false; break; }
-                            tc_fence_after();
-                        }
-                        const uint64_t kd = dk + (slot * kPiece >> 4);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_16_ss(tmem + t * kTile, q + (c * kPiece + k * 32 >> 4), kd + (k * 32 >> 4), id_s, c > 0 || k > 0);
-                        if (t == nt - 1) mma_commit(smem_u32(&sh.empty[slot]));
-                    }
-                    if (ok) mma_commit(smem_u32(&sh.s_full[t]));
+                const int g = j + 1;   // the key tile of the next scores
+                ready = false;
+                if (g < tiles) {
+                    if (t == 0 && !k_test(g) && !k_wait(g)) break;
+                    tc_fence_after();
+                    // the step after this one
+                    const int t1 = last_t ? 0 : 1, j1 = last_t ? g : j;
+                    scores(t, g, 0);
+                    const bool v_ready = j1 >= 0 && v_test(j1);
+                    scores(t, g, 1);
+                    ready = v_ready && mbar_test(smem_u32(&sh.p_full[t1][0]), j1 & 1);
+                    scores(t, g, 2);
+                    mma_commit(smem_u32(&sh.s_full[t]));
+                    if (last_t) mma_commit(smem_u32(&sh.k_empty[g & 1]));   // the last row tile frees K
                 }
             }
             mma_commit(smem_u32(&sh.mma_done));
@@ -249,13 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t == 0 && nk - kb < kTile) {
                     // value rows past the sequence's end: their weights are zero, but
                     // zero times a NaN is not. The rows are the next sequence's.
-                    const uint32_t v0 = j * kPerTile + 3;
-                    for (int c = 0; c < 2; ++c)
-                        hold(&sh.full[(v0 + c) % kSlots], ((v0 + c) / kSlots) & 1, ERR_WAIT_TMA_FULL);
+                    hold(&sh.v_full[j & 1], (j >> 1) & 1, ERR_WAIT_TMA_FULL);
                     const int left = nk - kb, per = (kTile - left) * 8;
                     for (int i = threadIdx.x; i < 2 * per; i += kTile) {
                         const int c = i >= per;
-                        st_shared_v4(sbase + kOffRing + ((v0 + c) % kSlots) * kPiece + left * 128 + (i - c * per) * 16,
+                        st_shared_v4(sbase + kOffRing + ((j * kPerTile + 3 + c) % kSlots) * kPiece + left * 128 + (i - c * per) * 16,
                                      make_uint4(0, 0, 0, 0));
                     }
                     fence_async_smem();
@@ -356,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    if (warp == 9) tmem_dealloc<512>(tmem);
+    if (warp == 9) tmem_dealloc<512>(sh.tmem);
 }
 
 template <typename T>
