@@ -35,7 +35,7 @@ static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 struct Shared {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];   // of every other key tile
-    uint64_t q_full, s_full[2], p_full[2][2], o_full[2], mma_done;
+    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], mma_done;
     uint32_t tmem;
     int abort;
 };
@@ -77,11 +77,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tiles = (keys + kTile - 1) / kTile;
 
     if (threadIdx.x == 0) {
-        mbar_init(smem_u32(&sh.q_full), 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&sh.k_full[t]), 1), mbar_init(smem_u32(&sh.k_empty[t]), 1);
             mbar_init(smem_u32(&sh.v_full[t]), 1), mbar_init(smem_u32(&sh.v_empty[t]), 1);
-            mbar_init(smem_u32(&sh.s_full[t]), 1);
+            mbar_init(smem_u32(&sh.q_full[t]), 1), mbar_init(smem_u32(&sh.s_full[t]), 1);
             mbar_init(smem_u32(&sh.p_full[t][0]), kTile), mbar_init(smem_u32(&sh.p_full[t][1]), kTile);
             mbar_init(smem_u32(&sh.o_full[t]), 1);
         }
@@ -107,11 +106,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // -------------------------------------------------------- loads
         if (lane == 0 && tiles > 0) {
             const uint64_t pol = policy_evict_normal();
-            mbar_arrive_expect_tx(smem_u32(&sh.q_full), (two ? 2 : 1) * kQPieces * kPiece);
-            for (int t = 0; t < (two ? 2 : 1); ++t)
+            auto load_q = [&](int t) {
+                mbar_arrive_expect_tx(smem_u32(&sh.q_full[t]), kQPieces * kPiece);
                 for (int c = 0; c < kQPieces; ++c)
-                    tma_load_3d(sbase + (t * kQPieces + c) * kPiece, &map_q, smem_u32(&sh.q_full), c * 64, h,
+                    tma_load_3d(sbase + (t * kQPieces + c) * kPiece, &map_q, smem_u32(&sh.q_full[t]), c * 64, h,
                                 static_cast<int>(q0) + r0 + t * kTile, pol);
+            };
+            load_q(0);
             int g = 0;
             for (; g < tiles; ++g) {
                 const int key = static_cast<int>(kk0) + g * kTile;
@@ -126,13 +127,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(smem_u32(&sh.v_empty[g & 1]), two_ago, ERR_WAIT_SMEM_EMPTY)) break;
                 tma_load_3d(dst(1), &map_kn, kf, 64, h, key, pol);
                 tma_load_2d(dst(2), &map_kp, kf, 0, key, pol);
+                if (g == 0 && two) load_q(1);
                 if (g > 0 && !wait(smem_u32(&sh.k_empty[(g - 1) & 1]), one_ago, ERR_WAIT_SMEM_EMPTY)) break;
                 mbar_arrive_expect_tx(vf, 2 * kPiece);
                 tma_load_3d(dst(3), &map_v, vf, 0, h, key, pol);
                 tma_load_3d(dst(4), &map_v, vf, 64, h, key, pol);
             }
             // the last loads must land before the CTA may exit
-            mbar_wait_drain(smem_u32(&sh.q_full), 0, a.err);
+            for (int t = 0; t < (two && g > 0 ? 2 : 1); ++t) mbar_wait_drain(smem_u32(&sh.q_full[t]), 0, a.err);
             for (int i = g < 2 ? 0 : g - 2; i < g; ++i) {
                 mbar_wait_drain(smem_u32(&sh.k_full[i & 1]), (i >> 1) & 1, a.err);
                 mbar_wait_drain(smem_u32(&sh.v_full[i & 1]), (i >> 1) & 1, a.err);
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // cache beside the softmax's code, and every turn of the loop cost 900 cycles.
             // A barrier test takes about 100 cycles and few MMAs are queued: the tests for
             // the next step are made between the present one's MMAs.
-            bool ok = wait(smem_u32(&sh.q_full), 0, ERR_WAIT_TMA_FULL), ready = false;
+            bool ok = true, ready = false;
             const int steps = tiles * nt;
 #pragma unroll 1
             for (int i = -nt; i < steps && ok; ++i) {
@@ -208,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int g = j + 1;   // the key tile of the next scores
                 ready = false;
                 if (g < tiles) {
+                    if (j < 0 && !wait(smem_u32(&sh.q_full[t]), 0, ERR_WAIT_TMA_FULL)) break;
                     if (t == 0 && !k_test(g) && !k_wait(g)) break;
                     tc_fence_after();
                     // the step after this one
@@ -338,7 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
-            T *dst = static_cast<T *>(a.out) + (q0 + row) * a.o_st + h * a.o_sh;
+            // Results leave through the row tile's query buffer (its scores are done): a
+            // thread holds a row, and rows are far apart in memory, so that 16-byte stores
+            // from registers would touch 32 lines each (4,000 cycles for the tile). From the
+            // buffer 16 lanes store a row's 256 bytes. Rows of 256 bytes, the 16-byte unit
+            // swizzled by the row; a warp keeps to its own 32 rows.
+            const uint32_t stage = sbase + t * kQPieces * kPiece + (warp & 3) * 32 * 256;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
@@ -349,16 +357,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0;
                 }
-                if (valid) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t w[4];
+                for (int i = 0; i < 32; i += 8) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = E::pack(__uint_as_float(o[i + 2 * k]) * inv, __uint_as_float(o[i + 2 * k + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(dst + c * 32 + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = E::pack(__uint_as_float(o[i + 2 * k]) * inv, __uint_as_float(o[i + 2 * k + 1]) * inv);
+                    st_shared_v4(stage + lane * 256 + (((c * 4 + i / 8) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
                 }
+            }
+            __syncwarp();
+            T *dst = static_cast<T *>(a.out) + (q0 + row - lane) * a.o_st + h * a.o_sh + (lane & 15) * 8;
+            const int left = nq - (row - lane);   // rows of the warp that exist
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const int r = i + (lane >> 4);
+                const uint4 v = ld_shared_v4(stage + r * 256 + (((lane & 15) ^ (r & 7)) << 4));
+                if (r < left) *reinterpret_cast<uint4 *>(dst + r * a.o_st) = v;
             }
             if (valid && a.lse)
                 a.lse[(q0 + row) * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
