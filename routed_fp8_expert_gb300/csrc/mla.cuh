@@ -156,6 +156,19 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Store a box of shared memory through a 3D tensor map (rows and columns past the
+// tensor's end are not written), and the issuing thread's waits: until its stores have
+// read shared memory, and until they are done.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // Two fp32 values in one 64-bit register pair: the packed fp32 instructions take one
 // issue slot for both.
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
@@ -322,8 +335,6 @@ struct RaggedArgs {
 };
 
 struct ProjArgs {
-    void *out;
-    int64_t o_st, o_sh;
     int T, H, K, N;
     int shared_x;             // x has one head that every output head reads
     unsigned int *err;
@@ -339,7 +350,7 @@ struct PagedMaps {
 cudaError_t launch_paged(const PagedMaps &m, const PagedArgs &a, bool bf16, int grid, cudaStream_t stream);
 cudaError_t launch_ragged(const CUtensorMap &q, const CUtensorMap &k_nope, const CUtensorMap &k_pe,
                           const CUtensorMap &v, const RaggedArgs &a, bool bf16, cudaStream_t stream);
-cudaError_t launch_proj(const CUtensorMap &x, const CUtensorMap &w, const ProjArgs &a, bool bf16, bool w_kn,
-                        int num_sms, cudaStream_t stream);
+cudaError_t launch_proj(const CUtensorMap &x, const CUtensorMap &w, const CUtensorMap &out, const ProjArgs &a, bool bf16,
+                        bool w_kn, int num_sms, cudaStream_t stream);
 
 }  // namespace moe

@@ -365,10 +365,14 @@ int mla_head_proj(const void *x, int64_t x_st, int64_t x_sh, int x_shared, const
     MLA_CHECK(stride(o_st, N, "o_st"));
     MLA_CHECK(stride(o_sh, H > 1 ? N : 8, "o_sh"));
     ProjArgs a{};
-    a.out = out, a.o_st = o_st, a.o_sh = o_sh;
     a.T = T, a.H = H, a.K = K, a.N = N, a.shared_x = x_shared;
     MLA_CUDA(device_error_word(&a.err), "error word address");
-    CUtensorMap mx, mw;
+    CUtensorMap mx, mw, mo;
+    {
+        const int64_t d[3] = {N, H, T}, s[2] = {o_sh, o_st};
+        const int box[3] = {64, 1, 32};
+        MLA_CHECK(tensor_map(&mo, out, dtype, 3, d, s, box, "out"));
+    }
     {
         const int64_t d[3] = {K, x_shared ? 1 : H, T}, s[2] = {x_shared ? x_st : x_sh, x_st};
         const int box[3] = {64, 1, 128};
@@ -379,7 +383,7 @@ int mla_head_proj(const void *x, int64_t x_st, int64_t x_sh, int x_shared, const
         const int box[3] = {64, w_kn ? 64 : 128, 1};
         MLA_CHECK(tensor_map(&mw, w, dtype, 3, d, s, box, "w"));
     }
-    MLA_CUDA(launch_proj(mx, mw, a, dtype == MLA_BF16, w_kn != 0, num_sms(), static_cast<cudaStream_t>(stream)),
+    MLA_CUDA(launch_proj(mx, mw, mo, a, dtype == MLA_BF16, w_kn != 0, num_sms(), static_cast<cudaStream_t>(stream)),
              "head projection launch");
     report_launches(1);
     return MOE_OK;
