@@ -7,7 +7,15 @@ namespace moe {
 __device__ unsigned int g_moe_device_error = 0;
 
 cudaError_t device_error_word(unsigned int **ptr) {
-    return cudaGetSymbolAddress(reinterpret_cast<void **>(ptr), g_moe_device_error);
+    // looked up once per device (the library's module stays loaded)
+    static std::atomic<unsigned int *> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*ptr = known[dev].load(std::memory_order_relaxed))) return cudaSuccess;
+    e = cudaGetSymbolAddress(reinterpret_cast<void **>(ptr), g_moe_device_error);
+    if (e == cudaSuccess && dev < 64) known[dev].store(*ptr, std::memory_order_relaxed);
+    return e;
 }
 
 template <Kind KIND, int BN>

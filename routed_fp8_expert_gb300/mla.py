@@ -36,19 +36,44 @@ def _index(t):
     return i
 
 
-def _ok(name, t, shape, dtype, index):
-    """Refuse a tensor of another shape, type, device or a strided innermost dimension."""
-    if t.shape == shape and t.dtype == dtype and t.get_device() == index and (shape[-1] < 2 or t.stride(-1) == 1):
-        return
+def _refuse(name, t, shape, dtype, index):
+    """Say what is wrong with a tensor of another shape, type, device or innermost stride."""
     if t.get_device() < 0:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.shape != shape:
+    if tuple(t.shape) != shape:
         _bad(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if t.dtype != dtype:
         _bad(f"{name} is {t.dtype}, expected {dtype}")
     if t.get_device() != index:
         _bad(f"{name} is on device {t.get_device()}, the call on {index}")
     _bad(f"the innermost dimension of {name} must be contiguous")
+
+
+# The argument forms: address (and outer strides) of a tensor that has to have the given
+# shape, type and device and a contiguous innermost dimension. A dimension of one may
+# carry any stride, so it gets a legal one.
+def _vec(name, t, n, dtype, index):
+    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != index or (n > 1 and t.stride(0) != 1):
+        _refuse(name, t, (n,), dtype, index)
+    return t.data_ptr()
+
+
+def _mat(name, t, n0, n1, dtype, index):
+    s0, s1 = t.stride() if t.dim() == 2 else (0, 0)
+    if t.shape != (n0, n1) or t.dtype is not dtype or t.get_device() != index or (s1 != 1 and n1 > 1):
+        _refuse(name, t, (n0, n1), dtype, index)
+    return t.data_ptr(), s0 if n0 > 1 else _pad8(n1)
+
+
+def _ten(name, t, n0, n1, n2, dtype, index):
+    s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.shape != (n0, n1, n2) or t.dtype is not dtype or t.get_device() != index or (s2 != 1 and n2 > 1):
+        _refuse(name, t, (n0, n1, n2), dtype, index)
+    if n1 <= 1:
+        s1 = _pad8(n2)
+    if n0 <= 1:
+        s0 = _pad8(max(n2, s1))
+    return t.data_ptr(), s0, s1
 
 
 def _code(name, t):
@@ -66,22 +91,6 @@ def _dims(name, t, n):
 
 def _pad8(n):
     return max(8, (n + 7) & ~7)
-
-
-def _row(t):
-    """Row stride of a matrix; a dimension of one may carry any stride, so it gets a legal one."""
-    return t.stride(0) if t.shape[0] > 1 else _pad8(t.shape[1])
-
-
-def _pair(t):
-    """The two outer strides of a 3D tensor, legal for dimensions of one."""
-    s0, s1, _ = t.stride()
-    n0, n1, w = t.shape
-    if n1 <= 1:
-        s1 = _pad8(w)
-    if n0 <= 1:
-        s0 = _pad8(max(w, s1))
-    return s0, s1
 
 
 @dataclass
@@ -123,51 +132,40 @@ def mla_rope_append(q_pe, kv, positions, plan: RopePlan, gamma=None, eps: float 
         _bad("q_pe and kv are both None")
     dev, ty, dim, T = _index(ref), ref.dtype, plan.dim, ref.shape[0]
     code = _code("q_pe" if q_pe is not None else "kv", ref)
-    H = 1
-    latent = pages = pq = pqo = pkv = pg = pko = pc = psl = q_st = q_sh = qo_st = qo_sh = 0
-    kv_st = ko_st = c_st = c_sr = 0
-    page = 1
+    H, page, latent, pages, gp, sp = 1, 1, 0, 0, None, None
+    qa = qo = (None, 0, 0)
+    ka = ko = (None, 0)
+    ca = (None, 0, 0)
     if q_pe is not None:
         H = _dims("q_pe", q_pe, 3)[1]
-        _ok("q_pe", q_pe, (T, H, dim), ty, dev)
+        qa = _ten("q_pe", q_pe, T, H, dim, ty, dev)
         if q_out is None:
             q_out = torch.empty((T, H, dim), dtype=ty, device=ref.device)
-        else:
-            _ok("q_out", q_out, (T, H, dim), ty, dev)
-        q_st, q_sh = _pair(q_pe)
-        qo_st, qo_sh = _pair(q_out)
-        pq, pqo = q_pe.data_ptr(), q_out.data_ptr()
+        qo = _ten("q_out", q_out, T, H, dim, ty, dev)
     elif q_out is not None:
         _bad("q_out is given without q_pe")
     if kv is not None:
         width = _dims("kv", kv, 2)[1]
         latent = width - dim
-        _ok("kv", kv, (T, width), ty, dev)
-        pkv, kv_st = kv.data_ptr(), _row(kv)
-        if kv_out is not None:
-            _ok("kv_out", kv_out, (T, width), ty, dev)
-        elif cache is None:
+        ka = _mat("kv", kv, T, width, ty, dev)
+        if kv_out is None and cache is None:
             kv_out = torch.empty((T, width), dtype=ty, device=ref.device)
         if kv_out is not None:
-            pko, ko_st = kv_out.data_ptr(), _row(kv_out)
+            ko = _mat("kv_out", kv_out, T, width, ty, dev)
         if gamma is not None:
-            _ok("gamma", gamma, (latent,), ty, dev)
-            pg = gamma.data_ptr()
+            gp = _vec("gamma", gamma, latent, ty, dev)
         if cache is not None:
             if slots is None:
                 _bad("cache is given without slots")
             pages, page, _ = _dims("cache", cache, 3)
-            _ok("cache", cache, (pages, page, width), ty, dev)
-            _ok("slots", slots, (T,), torch.int32, dev)
-            c_st, c_sr = _pair(cache)
-            pc, psl = cache.data_ptr(), slots.data_ptr()
+            ca = _ten("cache", cache, pages, page, width, ty, dev)
+            sp = _vec("slots", slots, T, torch.int32, dev)
     elif cache is not None or kv_out is not None:
         _bad("cache or kv_out is given without kv")
-    _ok("positions", positions, (T,), torch.int32, dev)
-    _ok("plan.freq", plan.freq, (dim // 2,), torch.int64, dev)
-    _check(load().mla_rope_append(pq, q_st, q_sh, pqo, qo_st, qo_sh, pkv, kv_st, pg, eps, pko, ko_st, pc, c_st, c_sr,
-                                  pages, page, psl, positions.data_ptr(), plan.freq.data_ptr(), plan.amplitude,
-                                  plan.layout, T, H, dim, latent, code, _raw_stream(dev)))
+    pp = _vec("positions", positions, T, torch.int32, dev)
+    fp = _vec("plan.freq", plan.freq, dim // 2, torch.int64, dev)
+    _check(load().mla_rope_append(*qa, *qo, *ka, gp, eps, *ko, *ca, pages, page, sp, pp, fp, plan.amplitude, plan.layout,
+                                  T, H, dim, latent, code, _raw_stream(dev)))
     return q_out, kv_out
 
 
@@ -190,26 +188,20 @@ def mla_attn_paged(q, cache, block_table, ctx_lens, scale: float, cu_q=None, out
     Tq, H, _ = _dims("q", q, 3)
     pages, page, _ = _dims("cache", cache, 3)
     B, max_pages = _dims("block_table", block_table, 2)
-    _ok("q", q, (Tq, H, width), ty, dev)
-    _ok("cache", cache, (pages, page, width), ty, dev)
-    _ok("block_table", block_table, (B, max_pages), torch.int32, dev)
-    _ok("ctx_lens", ctx_lens, (B,), torch.int32, dev)
-    if cu_q is not None:
-        _ok("cu_q", cu_q, (B + 1,), torch.int32, dev)
+    tp, t_st = _mat("block_table", block_table, B, max_pages, torch.int32, dev)
     if out is None:
         out = torch.empty((Tq, H, MLA_LATENT), dtype=ty, device=q.device)
-    else:
-        _ok("out", out, (Tq, H, MLA_LATENT), ty, dev)
     lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device) if want_lse else None
     if ws is None:
         ws = mla_paged_workspace(q.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         _bad("ws must be contiguous and on the call's device")
     _check(load().mla_attn_paged(
-        q.data_ptr(), *_pair(q), Tq, cache.data_ptr(), *_pair(cache), pages, page, block_table.data_ptr(),
-        block_table.stride(0) if B > 1 else max_pages, max_pages, ctx_lens.data_ptr(),
-        None if cu_q is None else cu_q.data_ptr(), B, H, scale, code, out.data_ptr(), *_pair(out),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, _raw_stream(dev)))
+        *_ten("q", q, Tq, H, width, ty, dev), Tq, *_ten("cache", cache, pages, page, width, ty, dev), pages, page, tp,
+        t_st if B > 1 else max_pages, max_pages, _vec("ctx_lens", ctx_lens, B, torch.int32, dev),
+        None if cu_q is None else _vec("cu_q", cu_q, B + 1, torch.int32, dev), B, H, scale, code,
+        *_ten("out", out, Tq, H, MLA_LATENT, ty, dev), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+        _raw_stream(dev)))
     return (out, lse) if want_lse else out
 
 
@@ -225,21 +217,15 @@ def mla_attn_ragged(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, scale: float, ca
     B = _dims("cu_q", cu_q, 1)[0] - 1
     if B < 0:
         _bad("cu_q is empty")
-    _ok("q", q, (Tq, H, MLA_NOPE + MLA_ROPE), ty, dev)
-    _ok("k_nope", k_nope, (Tk, H, MLA_NOPE), ty, dev)
-    _ok("k_pe", k_pe, (Tk, MLA_ROPE), ty, dev)
-    _ok("v", v, (Tk, H, MLA_V), ty, dev)
-    _ok("cu_q", cu_q, (B + 1,), torch.int32, dev)
-    _ok("cu_k", cu_k, (B + 1,), torch.int32, dev)
     if out is None:
         out = torch.empty((Tq, H, MLA_V), dtype=ty, device=q.device)
-    else:
-        _ok("out", out, (Tq, H, MLA_V), ty, dev)
     lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device) if want_lse else None
     _check(load().mla_attn_ragged(
-        q.data_ptr(), *_pair(q), Tq, k_nope.data_ptr(), *_pair(k_nope), k_pe.data_ptr(), _row(k_pe), v.data_ptr(),
-        *_pair(v), Tk, cu_q.data_ptr(), cu_k.data_ptr(), B, max_q, H, scale, 1 if causal else 0, code, out.data_ptr(),
-        *_pair(out), None if lse is None else lse.data_ptr(), _raw_stream(dev)))
+        *_ten("q", q, Tq, H, MLA_NOPE + MLA_ROPE, ty, dev), Tq, *_ten("k_nope", k_nope, Tk, H, MLA_NOPE, ty, dev),
+        *_mat("k_pe", k_pe, Tk, MLA_ROPE, ty, dev), *_ten("v", v, Tk, H, MLA_V, ty, dev), Tk,
+        _vec("cu_q", cu_q, B + 1, torch.int32, dev), _vec("cu_k", cu_k, B + 1, torch.int32, dev), B, max_q, H, scale,
+        1 if causal else 0, code, *_ten("out", out, Tq, H, MLA_V, ty, dev), None if lse is None else lse.data_ptr(),
+        _raw_stream(dev)))
     return (out, lse) if want_lse else out
 
 
@@ -253,12 +239,9 @@ def mla_head_proj(x, w, w_kn: bool = False, out=None):
     T, xh, _ = _dims("x", x, 3)
     if xh != 1 and xh != H:
         _bad(f"x has {xh} heads, w has {H}")
-    _ok("x", x, (T, xh, K), ty, dev)
-    _ok("w", w, (H, K, N) if w_kn else (H, N, K), ty, dev)
     if out is None:
         out = torch.empty((T, H, N), dtype=ty, device=x.device)
-    else:
-        _ok("out", out, (T, H, N), ty, dev)
-    _check(load().mla_head_proj(x.data_ptr(), *_pair(x), 1 if xh == 1 else 0, w.data_ptr(), *_pair(w),
-                                1 if w_kn else 0, T, H, K, N, code, out.data_ptr(), *_pair(out), _raw_stream(dev)))
+    wa = _ten("w", w, H, K, N, ty, dev) if w_kn else _ten("w", w, H, N, K, ty, dev)
+    _check(load().mla_head_proj(*_ten("x", x, T, xh, K, ty, dev), 1 if xh == 1 else 0, *wa, 1 if w_kn else 0, T, H, K, N,
+                                code, *_ten("out", out, T, H, N, ty, dev), _raw_stream(dev)))
     return out
