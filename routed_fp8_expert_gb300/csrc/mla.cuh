@@ -340,7 +340,7 @@ struct ProjArgs {
     unsigned int *err;
 };
 
-cudaError_t launch_rope(const RopeArgs &a, bool bf16, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs &a, bool bf16, cudaStream_t stream);
 // Tensor maps of mla_attn_paged: the queries; the cache in loads of two column groups
 // and of one.
 struct PagedMaps {

@@ -191,7 +191,7 @@ int mla_rope_append(const void *q, int64_t q_st, int64_t q_sh, void *q_out, int6
     a.T = T, a.H = H, a.dim = dim, a.latent = latent, a.layout = layout;
     a.amplitude = amplitude, a.eps = eps;
     MLA_CUDA(device_error_word(&a.err), "error word address");
-    MLA_CUDA(launch_rope(a, dtype == MLA_BF16, num_sms(), static_cast<cudaStream_t>(stream)), "rotary launch");
+    MLA_CUDA(launch_rope(a, dtype == MLA_BF16, static_cast<cudaStream_t>(stream)), "rotary launch");
     report_launches(1);
     return MOE_OK;
 }
