@@ -36,39 +36,74 @@ struct Shared {
     int abort;
 };
 
-// A CTA's part of the line, tile by tile.
+// A worker's (CTA's or pair's) part of the line, tile by tile. A tile is `rows` tokens of
+// `blocks` neighbouring weight blocks.
 struct Line {
-    int at, end, ntiles, ttiles;   // output tiles; feature tiles of a head; token tiles
-    int tt, n0, h;
-    bool first, last;              // of the run on one weight block
-    bool keep;                     // the block stays in shared memory over a run
+    int at, end, ttiles;   // tiles of the line; token tiles
+    int tt, block;         // the present tile: token tile, first weight block
+    bool first, last;      // of the run on one set of weight blocks
+    bool keep;             // the blocks stay in shared memory over a run
+    int blocks;
 
-    __device__ Line(const ProjArgs &a, int chunks) {
-        ntiles = (a.N + kTile - 1) / kTile;
-        ttiles = (a.T + kTile - 1) / kTile;
-        const int64_t total = static_cast<int64_t>(ttiles) * a.H * ntiles;
-        at = static_cast<int>(total * blockIdx.x / gridDim.x);
-        end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+    __device__ Line(const ProjArgs &a, int chunks, int worker, int workers, int rows, int blocks_) : blocks(blocks_) {
+        ttiles = (a.T + rows - 1) / rows;
+        const int64_t total = static_cast<int64_t>(ttiles) * (a.H * ntiles(a) / blocks);
+        at = static_cast<int>(total * worker / workers);
+        end = static_cast<int>(total * (worker + 1) / workers);
         keep = chunks <= kWSlots;
-        const int block = at / ttiles;
-        tt = at - block * ttiles;
-        h = block / ntiles;
-        n0 = (block - h * ntiles) * kTile;
+        const int g = at / ttiles;
+        tt = at - g * ttiles;
+        block = g * blocks;
         first = true;
         last = !keep || at + 1 == end || tt + 1 == ttiles;
     }
+    static __host__ __device__ int ntiles(const ProjArgs &a) { return (a.N + kTile - 1) / kTile; }
     __device__ bool more() const { return at < end; }
-    __device__ void next(const ProjArgs &a) {
+    __device__ void next() {
         ++at;
         first = !keep;
         if (++tt == ttiles) {
             tt = 0;
             first = true;
-            if ((n0 += kTile) >= a.N) n0 = 0, ++h;
+            block += blocks;
         }
         last = !keep || at + 1 == end || tt + 1 == ttiles;
     }
 };
+
+// One warp's 32 rows x 128 features of a tile, from the accumulator at `acc` through the
+// warp's 8 KB at `stage`: two boxes of 64 features with the 128-byte swizzle. TMA clips
+// rows past T and features past N.
+template <typename T>
+__device__ __forceinline__ void store_tile(const ProjArgs &a, const CUtensorMap *map_out, uint32_t acc, uint32_t stage,
+                                           int lane, int t, int block, bool ok) {
+    using E = Elem<T>;
+    if (lane == 0) tma_store_wait_read();   // the last boxes have left
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < kTile; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(acc + c, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                w[q] = E::pack(__uint_as_float(r[k + 2 * q]), __uint_as_float(r[k + 2 * q + 1]));
+            const int u = ((c & 32) + k) / 8;
+            st_shared_v4(stage + (c / 64) * 4096 + lane * 128 + ((u ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+        }
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0 && ok && t < a.T) {
+        const int nt = Line::ntiles(a), h = block / nt, n0 = (block - h * nt) * kTile;
+        tma_store_3d(map_out, stage, n0, h, t);
+        if (n0 + 64 < a.N) tma_store_3d(map_out, stage + 4096, n0 + 64, h, t);
+    }
+    if (lane == 0) tma_store_commit();
+}
 
 template <typename T, bool KN>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -107,7 +142,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t pol = policy_evict_normal();
             uint32_t xi = 0, wi = 0;   // chunks loaded
             bool ok = true;
-            for (Line l(a, chunks); l.more() && ok; l.next(a)) {
+            for (Line l(a, chunks, blockIdx.x, gridDim.x, kTile, 1); l.more() && ok; l.next()) {
+                const int nt = Line::ntiles(a), h = l.block / nt, n0 = (l.block - h * nt) * kTile;
                 for (int c = 0; c < chunks; ++c) {
                     if (l.first) {
                         const int st = wi % kWSlots;
@@ -116,10 +152,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(full, kChunk);
                         if (KN) {
                             // two boxes of 64 features x 64 K rows
-                            tma_load_3d(dst, &map_w, full, l.n0, c * 64, l.h, pol);
-                            tma_load_3d(dst + kChunk / 2, &map_w, full, l.n0 + 64, c * 64, l.h, pol);
+                            tma_load_3d(dst, &map_w, full, n0, c * 64, h, pol);
+                            tma_load_3d(dst + kChunk / 2, &map_w, full, n0 + 64, c * 64, h, pol);
                         } else {
-                            tma_load_3d(dst, &map_w, full, c * 64, l.n0, l.h, pol);
+                            tma_load_3d(dst, &map_w, full, c * 64, n0, h, pol);
                         }
                         ++wi;
                     }
@@ -127,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!wait(smem_u32(&sh.x_empty[st]), ((xi / kXSlots) & 1) ^ 1, ERR_WAIT_SMEM_EMPTY)) { ok = false; break; }
                     const uint32_t full = smem_u32(&sh.x_full[st]);
                     mbar_arrive_expect_tx(full, kChunk);
-                    tma_load_3d(sbase + kOffX + st * kChunk, &map_x, full, c * 64, a.shared_x ? 0 : l.h, l.tt * kTile, pol);
+                    tma_load_3d(sbase + kOffX + st * kChunk, &map_x, full, c * 64, a.shared_x ? 0 : h, l.tt * kTile, pol);
                     ++xi;
                 }
             }
@@ -147,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dw = KN ? sdesc_mn_sw128(sbase, kChunk / 2) : sdesc_sw128(sbase);
             uint32_t xi = 0, w0 = 0, n = 0;   // x chunks used; the block's first chunk; tiles
             bool ok = true;
-            for (Line l(a, chunks); l.more() && ok; l.next(a), ++n) {
+            for (Line l(a, chunks, blockIdx.x, gridDim.x, kTile, 1); l.more() && ok; l.next(), ++n) {
                 const uint32_t buf = n & 1;
                 if (!wait(smem_u32(&sh.acc_empty[buf]), ((n >> 1) & 1) ^ 1, ERR_WAIT_PART_EMPTY)) break;
 #pragma unroll 1
@@ -174,43 +210,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------- results
-        // A warp's 32 rows x 128 features: two boxes of 64 features with the 128-byte
-        // swizzle, in its own 8 KB.
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16, stage = sbase + kOffOut + warp * (kChunk / 2);
         uint32_t n = 0;
         bool ok = true;
-        for (Line l(a, chunks); l.more(); l.next(a), ++n) {
+        for (Line l(a, chunks, blockIdx.x, gridDim.x, kTile, 1); l.more(); l.next(), ++n) {
             const uint32_t buf = n & 1;
             if (ok) ok = wait(smem_u32(&sh.acc_full[buf]), (n >> 1) & 1, ERR_WAIT_PART_FULL);
             __syncwarp();
             tc_fence_after();
-            if (lane == 0) tma_store_wait_read();   // the last tile's boxes have left
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < kTile; c += 32) {
-                uint32_t r[32];
-                tmem_ld32(tmem + buf * kTile + lanes + c, r);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        w[q] = E::pack(__uint_as_float(r[k + 2 * q]), __uint_as_float(r[k + 2 * q + 1]));
-                    const int u = ((c & 32) + k) / 8;
-                    st_shared_v4(stage + (c / 64) * 4096 + lane * 128 + ((u ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
-                }
-            }
+            store_tile<T>(a, &map_out, tmem + buf * kTile + lanes, stage, lane, l.tt * kTile + warp * 32, l.block, ok);
             tc_fence_before();
             mbar_arrive(smem_u32(&sh.acc_empty[buf]));
-            fence_async_smem();
-            __syncwarp();
-            const int t = l.tt * kTile + warp * 32;
-            if (lane == 0 && ok && t < a.T) {
-                tma_store_3d(&map_out, stage, l.n0, l.h, t);
-                if (l.n0 + 64 < a.N) tma_store_3d(&map_out, stage + 4096, l.n0 + 64, l.h, t);
-            }
-            if (lane == 0) tma_store_commit();
         }
         if (lane == 0) tma_store_wait();
     }
@@ -218,15 +228,185 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 5) tmem_dealloc<256>(tmem);
 }
 
+// The same over CTA pairs for long inputs: tiles of 256 tokens x 256 features, of which
+// each CTA holds half of the tokens' rows, one of the two weight blocks and the results
+// of its rows. A CTA's chunk of x then feeds MMAs of twice the width, so that its ring of
+// four covers the loads' latency (1,700 cycles) at the tensor rate.
+struct PairShared {
+    uint64_t x_full[kXSlots], x_empty[kXSlots], w_full[kWSlots], w_empty[kWSlots], acc_full[2], acc_empty[2], mma_done;
+    uint32_t tmem;
+    int abort;
+};
+
+template <typename T, bool KN>
+__global__ void __launch_bounds__(kThreads, 1)
+    head_proj_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                          const __grid_constant__ CUtensorMap map_out, const ProjArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    PairShared &sh = *reinterpret_cast<PairShared *>(smem + kOffMisc);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    using E = Elem<T>;
+
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        // Full barriers are used at rank 0: its own arrival and both CTAs' bytes. Empty
+        // ones are used in each CTA, and a commit arrives at both. acc_empty, at rank 0,
+        // takes the result warps of both.
+        for (int i = 0; i < kXSlots; ++i) mbar_init(smem_u32(&sh.x_full[i]), 1), mbar_init(smem_u32(&sh.x_empty[i]), 1);
+        for (int i = 0; i < kWSlots; ++i) mbar_init(smem_u32(&sh.w_full[i]), 1), mbar_init(smem_u32(&sh.w_empty[i]), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.acc_full[i]), 1), mbar_init(smem_u32(&sh.acc_empty[i]), 8);
+        mbar_init(smem_u32(&sh.mma_done), 1);
+        sh.abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&map_x);
+        tma_prefetch_desc(&map_w);
+        tma_prefetch_desc(&map_out);
+    }
+    if (warp == 5) pair_tmem_alloc<512>(smem_u32(&sh.tmem));
+    tc_fence_before();
+    cluster_sync();   // both CTAs' barriers and tensor memory are ready
+    tc_fence_after();
+    constexpr uint32_t tmem = 0;   // all 512 columns of both CTAs
+    const Waiter wait{smem_u32(&sh.abort), a.err};
+    const int chunks = (a.K + 63) / 64;
+    auto line = [&] { return Line(a, chunks, blockIdx.x / 2, gridDim.x / 2, 2 * kTile, 2); };
+    pdl_wait();
+
+    if (warp == 4) {
+        // -------------------------------------------------------- loads (each CTA its own half)
+        if (elect_one()) {
+            const uint64_t pol = policy_evict_normal();
+            uint32_t xi = 0, wi = 0;   // chunks loaded
+            bool ok = true;
+            for (Line l = line(); l.more() && ok; l.next()) {
+                const int nt = Line::ntiles(a), block = l.block + rank, h = block / nt, n0 = (block - h * nt) * kTile;
+                for (int c = 0; c < chunks; ++c) {
+                    if (l.first) {
+                        const int st = wi % kWSlots;
+                        if (!wait(smem_u32(&sh.w_empty[st]), ((wi / kWSlots) & 1) ^ 1, ERR_WAIT_SMEM_EMPTY)) { ok = false; break; }
+                        const uint32_t full = rank0_address(smem_u32(&sh.w_full[st])), dst = sbase + st * kChunk;
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.w_full[st]), 2 * kChunk);
+                        if (KN) {
+                            pair_load_3d(dst, &map_w, full, n0, c * 64, h, pol);
+                            pair_load_3d(dst + kChunk / 2, &map_w, full, n0 + 64, c * 64, h, pol);
+                        } else {
+                            pair_load_3d(dst, &map_w, full, c * 64, n0, h, pol);
+                        }
+                        ++wi;
+                    }
+                    const int st = xi % kXSlots;
+                    if (!wait(smem_u32(&sh.x_empty[st]), ((xi / kXSlots) & 1) ^ 1, ERR_WAIT_SMEM_EMPTY)) { ok = false; break; }
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.x_full[st]), 2 * kChunk);
+                    pair_load_3d(sbase + kOffX + st * kChunk, &map_x, rank0_address(smem_u32(&sh.x_full[st])), c * 64,
+                                 a.shared_x ? 0 : h, (2 * l.tt + static_cast<int>(rank)) * kTile, pol);
+                    ++xi;
+                }
+            }
+            // the last loads of both must land before either may exit
+            if (rank == 0) {
+                for (uint32_t i = xi < kXSlots ? 0 : xi - kXSlots; i < xi; ++i)
+                    mbar_wait_drain(smem_u32(&sh.x_full[i % kXSlots]), (i / kXSlots) & 1, a.err);
+                for (uint32_t i = wi < kWSlots ? 0 : wi - kWSlots; i < wi; ++i)
+                    mbar_wait_drain(smem_u32(&sh.w_full[i % kWSlots]), (i / kWSlots) & 1, a.err);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // -------------------------------------------------------- MMA issue (rank 0, for both)
+        if (rank == 0 && elect_one()) {
+            const IssueWaiter wait{smem_u32(&sh.abort), a.err};
+            constexpr uint32_t id = idesc16(E::kFmt, 2 * kTile, 2 * kTile, false, KN);
+            const uint64_t dx = sdesc_sw128(sbase + kOffX);
+            const uint64_t dw = KN ? sdesc_mn_sw128(sbase, kChunk / 2) : sdesc_sw128(sbase);
+            uint32_t xi = 0, w0 = 0, n = 0;   // x chunks used; the blocks' first chunk; tiles
+            bool ok = true;
+            for (Line l = line(); l.more() && ok; l.next(), ++n) {
+                const uint32_t buf = n & 1;
+                if (!wait(smem_u32(&sh.acc_empty[buf]), ((n >> 1) & 1) ^ 1, ERR_WAIT_PART_EMPTY)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c, ++xi) {
+                    const uint32_t wi = w0 + c, ws = wi % kWSlots, xs = xi % kXSlots;
+                    if (l.first && !wait(smem_u32(&sh.w_full[ws]), (wi / kWSlots) & 1, ERR_WAIT_TMA_FULL)) { ok = false; break; }
+                    if (!wait(smem_u32(&sh.x_full[xs]), (xi / kXSlots) & 1, ERR_WAIT_TMA_FULL)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t xd = dx + (xs * kChunk >> 4), wd = dw + (ws * kChunk >> 4);
+                    const uint32_t acc0 = c > 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        pair_mma_16_ss(tmem + buf * 2 * kTile, xd + (k * 32 >> 4), wd + (KN ? k * 2048 >> 4 : k * 32 >> 4), id,
+                                       k > 0 ? 1 : acc0);
+                    pair_commit(smem_u32(&sh.x_empty[xs]));
+                    if (l.last) pair_commit(smem_u32(&sh.w_empty[ws]));
+                }
+                if (!ok) break;
+                pair_commit(smem_u32(&sh.acc_full[buf]));
+                if (l.last) w0 += chunks;
+            }
+            pair_commit(smem_u32(&sh.mma_done));
+            mbar_wait_drain(smem_u32(&sh.mma_done), 0, a.err);
+        }
+        __syncwarp();
+    } else {
+        // -------------------------------------------------------- results (each CTA its rows)
+        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16, stage = sbase + kOffOut + warp * (kChunk / 2);
+        uint32_t n = 0;
+        bool ok = true;
+        for (Line l = line(); l.more(); l.next(), ++n) {
+            const uint32_t buf = n & 1;
+            if (ok) ok = wait(smem_u32(&sh.acc_full[buf]), (n >> 1) & 1, ERR_WAIT_PART_FULL);
+            __syncwarp();
+            tc_fence_after();
+            const int t = (2 * l.tt + static_cast<int>(rank)) * kTile + warp * 32;
+            for (int b = 0; b < 2; ++b)
+                store_tile<T>(a, &map_out, tmem + (2 * buf + b) * kTile + lanes, stage, lane, t, l.block + b, ok);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t bar = rank0_address(smem_u32(&sh.acc_empty[buf]));
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+            }
+        }
+        if (lane == 0) tma_store_wait();
+    }
+    __syncwarp();
+    cluster_sync();   // neither CTA leaves while the other may reach its memory
+    if (warp == 5) pair_tmem_dealloc<512>(sh.tmem);
+}
+
+// Pairs take two weight blocks that read the same x: an even number of a head's, or of all
+// when the heads share x. They win where a run is long enough to be bound by the tensor
+// rate; below, 128-token tiles spread over twice as many workers.
+bool use_pairs(const ProjArgs &a) {
+    const int nt = Line::ntiles(a);
+    return a.T > 1024 && (a.shared_x ? a.H * nt : nt) % 2 == 0;
+}
+
 template <typename T, bool KN>
 cudaError_t launch_t(const CUtensorMap &x, const CUtensorMap &w, const CUtensorMap &out, const ProjArgs &a, int num_sms,
                      cudaStream_t stream) {
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(head_proj_kernel<T, KN>, kSmem, done);
+    const bool pairs = use_pairs(a);
+    auto kernel = pairs ? head_proj_pair_kernel<T, KN> : head_proj_kernel<T, KN>;
+    static std::atomic<uint64_t> done[2];
+    cudaError_t e = allow_smem(kernel, kSmem, done[pairs]);
     if (e != cudaSuccess) return e;
-    const int64_t total = static_cast<int64_t>((a.T + kTile - 1) / kTile) * a.H * ((a.N + kTile - 1) / kTile);
-    const int grid = total < num_sms ? static_cast<int>(total) : num_sms;
-    return launch_pdl(head_proj_kernel<T, KN>, dim3(grid), dim3(kThreads), kSmem, stream, x, w, out, a);
+    const int per = pairs ? 2 : 1, workers = num_sms / per;
+    const int64_t total = static_cast<int64_t>((a.T + per * kTile - 1) / (per * kTile)) * (a.H * Line::ntiles(a) / per);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(per * (total < workers ? static_cast<int>(total) : workers));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = per;
+    return cudaLaunchKernelEx(&cfg, kernel, x, w, out, a);
 }
 
 }  // namespace

@@ -46,6 +46,27 @@ def test_head_proj(T, H, K, N, shared, w_kn, dtype):
     check(y, ref, rounding(dtype, ref) + (K / 16 + 8) * 2.0 ** -23 * mag, "out")
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("w_kn", [False, True])
+@pytest.mark.parametrize("T,H,K,N,shared", [
+    (1025, 3, 512, 256, False), (1100, 2, 128, 512, False), (2000, 5, 640, 240, False), (1153, 4, 512, 128, True),
+    (1281, 3, 72, 128, True), (3001, 1, 8, 136, False),
+])
+def test_head_proj_of_long_inputs(T, H, K, N, shared, w_kn, dtype):
+    # pairs of CTAs (an even number of weight blocks that read the same x), or the
+    # 128-token tiles where the number is odd
+    x = randn(T, 1 if shared else H, K, seed=T, dtype=dtype)
+    w = randn(*((H, K, N) if w_kn else (H, N, K)), seed=K, dtype=dtype, std=K ** -0.5)
+    buf = torch.full((T + 1, H, N + 8), 3.0, dtype=dtype, device=DEV)
+    y = moe.mla_head_proj(x.to(DEV), w.to(DEV), w_kn=w_kn, out=buf[:T, :, :N])
+    assert error_word() == (_lib.MOE_OK, 0)
+    xd, wd = x.double().expand(T, H, K), w.double() if w_kn else w.double().transpose(1, 2)
+    ref = torch.einsum("thk,hkn->thn", xd, wd)
+    mag = torch.einsum("thk,hkn->thn", xd.abs(), wd.abs())
+    check(y, ref, rounding(dtype, ref) + (K / 16 + 8) * 2.0 ** -23 * mag, "out")
+    assert (buf[T] == 3.0).all() and (buf[:, :, N:] == 3.0).all()
+
+
 def test_head_proj_reads_views_in_place():
     # one up-projection weight [H, 256, 512] holds the key and the value halves of each
     # head; the absorb product reads the key half with K contiguous rows swapped
