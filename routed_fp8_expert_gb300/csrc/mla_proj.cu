@@ -12,7 +12,7 @@ namespace {
 // chunks of 64. The tiles form one line, token tiles fastest, cut evenly over the CTAs:
 // a CTA meets runs of token tiles of one weight block [128 features, K] and loads the
 // block once per run (K up to 512 stays in its ring of eight 16 KB chunks; longer
-// blocks pass through it for every tile). x passes through a ring of four. Streaming
+// blocks pass through it for every tile). x passes through a ring of five. Streaming
 // both operands for every tile would take 124 bytes per cycle and SM from L2 at the
 // tensor rate, twice what it delivers; x alone takes 62.
 // The accumulator is doubled in tensor memory, so that one tile's results leave (shared
@@ -21,11 +21,11 @@ namespace {
 // copy, transposes it. Chunks past K, rows past T and columns past N arrive as zeros.
 constexpr int kTile = 128;
 constexpr int kChunk = kTile * 128;      // 16 KB: 128 rows of 64 values
-constexpr int kXSlots = 4;
+constexpr int kXSlots = 5;
 constexpr int kWSlots = 8;
 constexpr int kOffX = kWSlots * kChunk;
 constexpr int kOffOut = kOffX + kXSlots * kChunk;
-constexpr int kOffMisc = kOffOut + 2 * kChunk;
+constexpr int kOffMisc = kOffOut + kChunk;
 constexpr int kSmem = kOffMisc + 1024;
 constexpr int kThreads = 192;            // four result warps, loads, MMA
 static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -72,37 +72,36 @@ struct Line {
 };
 
 // One warp's 32 rows x 128 features of a tile, from the accumulator at `acc` through the
-// warp's 8 KB at `stage`: two boxes of 64 features with the 128-byte swizzle. TMA clips
-// rows past T and features past N.
+// warp's 4 KB at `stage`: boxes of 64 features with the 128-byte swizzle. TMA clips rows
+// past T and features past N.
 template <typename T>
 __device__ __forceinline__ void store_tile(const ProjArgs &a, const CUtensorMap *map_out, uint32_t acc, uint32_t stage,
                                            int lane, int t, int block, bool ok) {
     using E = Elem<T>;
-    if (lane == 0) tma_store_wait_read();   // the last boxes have left
-    __syncwarp();
+    const int nt = Line::ntiles(a), h = block / nt, n0 = (block - h * nt) * kTile;
 #pragma unroll
-    for (int c = 0; c < kTile; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(acc + c, r);
-        tmem_wait_ld();
+    for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-            uint32_t w[4];
+        for (int c = 0; c < 2; ++c) {
+            uint32_t r[32];
+            tmem_ld32(acc + half * 64 + c * 32, r);
+            tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                w[q] = E::pack(__uint_as_float(r[k + 2 * q]), __uint_as_float(r[k + 2 * q + 1]));
-            const int u = ((c & 32) + k) / 8;
-            st_shared_v4(stage + (c / 64) * 4096 + lane * 128 + ((u ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+            for (int k = 0; k < 16; ++k) w[c * 16 + k] = E::pack(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+        }
+        if (lane == 0) tma_store_wait_read();   // the last box has left
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            st_shared_v4(stage + lane * 128 + ((u ^ (lane & 7)) << 4), make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (ok && t < a.T && n0 + half * 64 < a.N) tma_store_3d(map_out, stage, n0 + half * 64, h, t);
+            tma_store_commit();
         }
     }
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0 && ok && t < a.T) {
-        const int nt = Line::ntiles(a), h = block / nt, n0 = (block - h * nt) * kTile;
-        tma_store_3d(map_out, stage, n0, h, t);
-        if (n0 + 64 < a.N) tma_store_3d(map_out, stage + 4096, n0 + 64, h, t);
-    }
-    if (lane == 0) tma_store_commit();
 }
 
 template <typename T, bool KN>
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------- results
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16, stage = sbase + kOffOut + warp * (kChunk / 2);
+        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16, stage = sbase + kOffOut + warp * (kChunk / 4);
         uint32_t n = 0;
         bool ok = true;
         for (Line l(a, chunks, blockIdx.x, gridDim.x, kTile, 1); l.more(); l.next(), ++n) {
@@ -231,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The same over CTA pairs for long inputs: tiles of 256 tokens x 256 features, of which
 // each CTA holds half of the tokens' rows, one of the two weight blocks and the results
 // of its rows. A CTA's chunk of x then feeds MMAs of twice the width, so that its ring of
-// four covers the loads' latency (1,700 cycles) at the tensor rate.
+// five covers the loads' latency (1,700 cycles) at the tensor rate.
 struct PairShared {
     uint64_t x_full[kXSlots], x_empty[kXSlots], w_full[kWSlots], w_empty[kWSlots], acc_full[2], acc_empty[2], mma_done;
     uint32_t tmem;
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------- results (each CTA its rows)
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16, stage = sbase + kOffOut + warp * (kChunk / 2);
+        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16, stage = sbase + kOffOut + warp * (kChunk / 4);
         uint32_t n = 0;
         bool ok = true;
         for (Line l = line(); l.more(); l.next(), ++n) {
@@ -377,11 +376,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Pairs take two weight blocks that read the same x: an even number of a head's, or of all
-// when the heads share x. They win where a run is long enough to be bound by the tensor
-// rate; below, 128-token tiles spread over twice as many workers.
+// when the heads share x. They win where the tensor rate bounds the call (from 350 flops
+// per byte; the GPU's own ratio is 270): 4096 tokens of 512 -> 64 x 256, shared, 66 -> 51
+// us. Where memory bounds it they lose to the 128-token tiles, which spread over twice as
+// many workers: 4096 tokens of 64 heads, 128 -> 512, 95 against 83 us.
 bool use_pairs(const ProjArgs &a) {
     const int nt = Line::ntiles(a);
-    return a.T > 1024 && (a.shared_x ? a.H * nt : nt) % 2 == 0;
+    const double T = a.T, H = a.H, K = a.K, N = a.N;
+    const double bytes = 2.0 * (T * K * (a.shared_x ? 1.0 : H) + H * K * N + T * H * N);
+    return (a.shared_x ? a.H * nt : nt) % 2 == 0 && 2.0 * T * H * K * N > 350.0 * bytes;
 }
 
 template <typename T, bool KN>
