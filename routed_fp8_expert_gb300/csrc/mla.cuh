@@ -385,6 +385,7 @@ struct RaggedArgs {
 struct ProjArgs {
     int T, H, K, N;
     int shared_x;             // x has one head that every output head reads
+    int x_rows;               // rows of one load of x
     unsigned int *err;
 };
 

@@ -366,6 +366,10 @@ int mla_head_proj(const void *x, int64_t x_st, int64_t x_sh, int x_shared, const
     MLA_CHECK(stride(o_sh, H > 1 ? N : 8, "o_sh"));
     ProjArgs a{};
     a.T = T, a.H = H, a.K = K, a.N = N, a.shared_x = x_shared;
+    // no more rows than the call has, up to the next power of two: rows past T would cost a
+    // request each, and all CTAs' at the same place when the heads share x (one token,
+    // 512 -> 64 x 256, 20.7 us with 128-row loads)
+    for (a.x_rows = 128; a.x_rows > 8 && a.x_rows / 2 >= T;) a.x_rows /= 2;
     MLA_CUDA(device_error_word(&a.err), "error word address");
     CUtensorMap mx, mw, mo;
     {
@@ -375,7 +379,7 @@ int mla_head_proj(const void *x, int64_t x_st, int64_t x_sh, int x_shared, const
     }
     {
         const int64_t d[3] = {K, x_shared ? 1 : H, T}, s[2] = {x_shared ? x_st : x_sh, x_st};
-        const int box[3] = {64, 1, 128};
+        const int box[3] = {64, 1, a.x_rows};
         MLA_CHECK(tensor_map(&mx, x, dtype, 3, d, s, box, "x"));
     }
     {

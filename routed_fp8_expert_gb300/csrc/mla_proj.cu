@@ -161,7 +161,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int st = xi % kXSlots;
                     if (!wait(smem_u32(&sh.x_empty[st]), ((xi / kXSlots) & 1) ^ 1, ERR_WAIT_SMEM_EMPTY)) { ok = false; break; }
                     const uint32_t full = smem_u32(&sh.x_full[st]);
-                    mbar_arrive_expect_tx(full, kChunk);
+                    // (a short call loads only its rows: what the rest of the tile holds
+                    // reaches only results that are not stored)
+                    mbar_arrive_expect_tx(full, a.x_rows * 128);
                     tma_load_3d(sbase + kOffX + st * kChunk, &map_x, full, c * 64, a.shared_x ? 0 : h, l.tt * kTile, pol);
                     ++xi;
                 }
