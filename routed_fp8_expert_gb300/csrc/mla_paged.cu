@@ -343,11 +343,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kMaxSubs; ++i) {
                     if (i >= subs) break;
-                    // a box past the last key reads zeros (its page lies past the cache)
-                    const bool bad = static_cast<uint32_t>(cur.page[i]) >= static_cast<uint32_t>(a.num_pages);
-                    if (bad && cur.page[i] != kNoPage) record_error(a.err, ERR_BAD_INDEX);
-                    z[i] = bad ? static_cast<int>(a.num_pages) : cur.page[i];
-                    y[i] = cur.row[i];
+                    // A box past the last key repeats the tile's first: its scores are masked and
+                    // its values cleared, whereas a box outside the cache would cost a request
+                    // per row, all CTAs' at one place. A page that is not one reads zeros.
+                    const bool none = cur.page[i] == kNoPage;
+                    const bool bad = !none && static_cast<uint32_t>(cur.page[i]) >= static_cast<uint32_t>(a.num_pages);
+                    if (bad) record_error(a.err, ERR_BAD_INDEX);
+                    z[i] = none ? z[0] : bad ? static_cast<int>(a.num_pages) : cur.page[i];
+                    y[i] = none ? y[0] : cur.row[i];
                 }
                 more = cur.step(a);
                 const uint32_t turn = tile >> 1;   // earlier uses of this half of the ring
@@ -398,11 +401,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (w.tiles() > 0) {
                     const uint32_t full = smem_u32(&sh.q_full);
                     if (!wait(smem_u32(&sh.q_empty), (seg & 1) ^ 1, ERR_WAIT_SMEM_EMPTY)) break;
-                    mbar_arrive_expect_tx(full, kQBytes);
-                    const int r0 = w.rt * kRows;
+                    // rows past the sequence keep what the buffer held: their weights are zero
+                    const int r0 = w.rt * kRows, rows = min(kRows, w.s.n * a.H - r0);
+                    mbar_arrive_expect_tx(full, rows * kMlaWidth * 2);
                     int t = r0 / a.H, h = r0 - t * a.H;
-                    for (int r = 0; r < kRows; r += a.q_box) {
-                        // rows past the sequence are the next one's (or zero): computed, not kept
+                    for (int r = 0; r < rows; r += a.q_box) {
                         if (a.q_box == kRows) {
                             tma_load_4d(sbase, &maps.q, full, 0, h, 0, w.s.row0 + t, pol);
                         } else {
