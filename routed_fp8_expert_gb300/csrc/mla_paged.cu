@@ -577,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         hold(&sh.pv_done, (tile - 1) & 1, ERR_WAIT_PART_FULL);
                         tc_fence_after();
                         named_bar_sync(1, kSoftThreads);
+#pragma unroll 1
                         for (int c = half * 2 * kRows; c < (half + 1) * 2 * kRows; c += 32) {
                             uint32_t o[32];
                             tmem_ld32(tmem + kTmemO + c + lane_base, o);
@@ -663,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t stage = sbase + kOffP + warp * 1024;
                 const uint32_t st_row = lane & 7, st_chunk = lane >> 3;
                 T *out = static_cast<T *>(a.out) + quad * 32 + (lane & 3) * 8;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 2 * kRows; c += 32) {
                     uint32_t o0[16], o1[16];
                     if (n > 0) {
@@ -702,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 float *part = a.part_o + static_cast<int64_t>(slot) * kRows * kMlaLatent + quad * 32 + lane;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 2 * kRows; c += 32) {
                     uint32_t o[32];
                     if (n > 0) {
@@ -787,6 +788,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
     // rows before join c, of the joins of few parts and of many
     __shared__ int s_rows[2][kMaxCtas + 1];
     __shared__ int s_sum[2][kMaxCtas / 32];
+    __shared__ int4 s_join[kMaxCtas];
     __shared__ float4 s_acc[3][4][32];
     __shared__ float2 s_ml[4];
     pdl_trigger();
@@ -797,6 +799,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
     {
         const int c = tid % kMaxCtas;
         const int4 j = c < ctas ? a.joins[c] : make_int4(0, 0, 0, 0);
+        if (tid < kMaxCtas) s_join[c] = j;
         const int joins = __syncthreads_count(tid < kMaxCtas && j.z > 0);
         const bool many = j.w - c + 1 > (joins > kFewJoins ? 32 : kAhead);
         rows = many == (tid >= kMaxCtas) ? j.z : 0;
@@ -835,7 +838,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
     };
     for (int i = (kJoinThreads / 32) * blockIdx.x + warp; i < s_rows[0][kMaxCtas]; i += (kJoinThreads / 32) * gridDim.x) {
         const int c = find(0, i), r = i - s_rows[0][c];
-        const int4 j = a.joins[c];
+        const int4 j = s_join[c];
         const int parts = j.w - c + 1;
         auto slot_of = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * kRows + r; };
         auto sums_of = [&](int s, int k) {
@@ -874,7 +877,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
     }
     for (int i = blockIdx.x; i < s_rows[1][kMaxCtas]; i += gridDim.x) {
         const int c = find(1, i), r = i - s_rows[1][c];
-        const int4 j = a.joins[c];
+        const int4 j = s_join[c];
         const int parts = j.w - c + 1, per = (parts + 3) / 4;
         auto slot_of = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * kRows + r; };
         float M, L;
