@@ -53,6 +53,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     using E = Elem<T>;
 
     pdl_trigger();
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_kn);
+        tma_prefetch_desc(&map_kp);
+        tma_prefetch_desc(&map_v);
+    }
     pdl_wait();
     // the longest rows first: they see the most keys
     const int qt = gridDim.x - 1 - blockIdx.x;
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j > 0) {
                         // S_t of this tile was issued after P_t V of the one before, and
                         // its completion covers both: O_t is at rest
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t o[32];
                             tmem_ld32(to + c * 32, o);
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // buffer 16 lanes store a row's 256 bytes. Rows of 256 bytes, the 16-byte unit
             // swizzled by the row; a warp keeps to its own 32 rows.
             const uint32_t stage = sbase + t * kQPieces * kPiece + (warp & 3) * 32 * 256;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
                 if (tiles > 0) {
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             T *dst = static_cast<T *>(a.out) + (q0 + row - lane) * a.o_st + h * a.o_sh + (lane & 15) * 8;
             const int left = nq - (row - lane);   // rows of the warp that exist
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < 32; i += 2) {
                 const int r = i + (lane >> 4);
                 const uint4 v = ld_shared_v4(stage + r * 256 + (((lane & 15) ^ (r & 7)) << 4));
