@@ -286,6 +286,30 @@ def test_paged_views_and_strides():
     assert torch.equal(got, base) and torch.equal(lse, lse0) and (out[..., 512:] == 5.0).all()
 
 
+def test_offsets_past_32_bits():
+    # pages whose element offsets pass 2^32: appended to, then read
+    page, pages = 64, 120_000
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("needs 9 GB for the cache")
+    cache = torch.empty(pages, page, 576, dtype=BF16, device=DEV)
+    assert cache.numel() > 2 ** 32
+    n, last = 200, pages - 1
+    kv, pos = randn(n, 576, seed=1).to(DEV), torch.arange(n, dtype=torch.int32, device=DEV)
+    table = torch.tensor([[last, 0, last - 7, last - 1]], dtype=torch.int32)
+    slots = torch.cat([torch.arange(p * page, (p + 1) * page) for p in table[0].tolist()])[:n].to(torch.int32)
+    plan = moe.rope_plan(64, device=DEV)
+    _, rows = moe.mla_rope_append(None, kv, pos, plan, cache=cache, slots=slots.to(DEV),
+                                  kv_out=torch.empty(n, 576, dtype=BF16, device=DEV))
+    q = randn(1, 64, 576, seed=2)
+    o, lse = moe.mla_attn_paged(q.to(DEV), cache, table.to(DEV), torch.tensor([n], dtype=torch.int32, device=DEV), SCALE,
+                                want_lse=True)
+    assert error_word() == (_lib.MOE_OK, 0)
+    keys = rows.cpu()
+    ro, rl, ob, lb = attention(q[0], keys, keys[:, :512], [n] * 64, SCALE, BF16)
+    check(o[0], ro, ob, "out")
+    check(lse[0], rl, lb, "lse")
+
+
 def test_paged_many_sequences():
     # more sequences than the start-up scan takes at once
     ctx = [(37 * i) % 150 for i in range(500)]
@@ -433,6 +457,65 @@ def test_ragged_bad_offsets_are_reported_and_skipped():
 
 
 # ------------------------------------------------------------- streams, both forms
+
+def test_absorbed_and_expanded_forms_agree():
+    # one prompt through both forms: c -> W_ukv -> expanded attention, and W_uk^T q ->
+    # absorbed attention over the cache -> W_uv; differently rounded, the same attention
+    n, H, page = 150, 8, 64
+    w = randn(H, 256, 512, seed=1, std=512 ** -0.5).to(DEV)
+    q, kv = randn(n, H, 192, seed=2).to(DEV), randn(n, 576, seed=3, std=2.0).to(DEV)
+    gamma = (1 + 0.1 * randn(512, seed=4).float()).to(BF16).to(DEV)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    plan = moe.rope_plan(64, 50000.0, 32.0, mscale_all_dim=1.0, device=DEV)
+    scale = SCALE * plan.softmax_factor
+    cache = torch.zeros(4, page, 576, dtype=BF16, device=DEV)
+    q_abs, row = torch.empty(n, H, 576, dtype=BF16, device=DEV), torch.empty(n, 576, dtype=BF16, device=DEV)
+    q_rot = q.clone()
+    moe.mla_rope_append(q[..., 128:], kv, pos, plan, gamma=gamma, cache=cache, slots=pos + 64,
+                        q_out=q_abs[..., 512:], kv_out=row)
+    q_rot[..., 128:] = q_abs[..., 512:]
+    kvx = moe.mla_head_proj(row[:, None, :512], w)
+    cu = offsets([n])
+    expanded = moe.mla_attn_ragged(q_rot, kvx[..., :128], row[:, 512:], kvx[..., 128:], cu, cu, n, scale)
+    moe.mla_head_proj(q[..., :128], w[:, :128], w_kn=True, out=q_abs[..., :512])
+    table = torch.tensor([[1, 2, 3]], dtype=torch.int32, device=DEV)
+    o = moe.mla_attn_paged(q_abs, cache, table, torch.tensor([n], dtype=torch.int32, device=DEV), scale, cu_q=cu)
+    absorbed = moe.mla_head_proj(o, w[:, 128:])
+    # the 64-bit form of the same roundings-free attention, from the shared inputs
+    c, kp = row[:, :512].double().cpu(), row[:, 512:].double().cpu()
+    wd, qd = w.double().cpu(), q_rot.double().cpu()
+    k = torch.einsum("sc,hnc->shn", c, wd)
+    u = 2.0 ** -8
+    for h in range(H):
+        s = (qd[:, h, :128] @ k[:, h, :128].T + qd[:, h, 128:] @ kp.T) * scale
+        s = s.masked_fill(torch.ones(n, n).triu(1).bool(), -math.inf)
+        p = torch.softmax(s, 1)
+        ref, mag = p @ k[:, h, 128:], p @ k[:, h, 128:].abs()
+        # one rounding of every factor of a score (q', or k), of a weight, of a value and of
+        # a result: the scores' error reaches every weight
+        e = 2 * u * scale * (qd[:, h].abs() @ torch.cat((k[:, h, :128], kp), 1).abs().T).max(1).values[:, None]
+        big = torch.einsum("tc,cn->tn", (p.abs() @ c.abs()), wd[h, 128:].abs().T)   # sums of the absorbed form's terms
+        check(expanded[:, h], ref, 4 * u * mag + 2 * e * mag, "expanded")
+        q_lat = qd[:, h, :128].abs() @ wd[h, :128].abs()
+        e_abs = 2 * u * scale * ((q_lat @ c.abs().T) + qd[:, h, 128:].abs() @ kp.abs().T).max(1).values[:, None]
+        check(absorbed[:, h], ref, 4 * u * big + 2 * e_abs * mag, "absorbed")
+
+
+def test_two_streams_with_a_workspace_each():
+    q, cache, table, ctx_t = paged_inputs([5000, 40, 900], [1] * 3, 64, 64, seed=21)
+    args = [x.to(DEV) for x in (q, cache, table, ctx_t)]
+    want = moe.mla_attn_paged(*args, SCALE)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    ws = [moe.mla_paged_workspace(DEV) for _ in streams]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(moe.mla_attn_paged(*args, SCALE, ws=ws[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs[0] + outs[1])
 
 def test_on_another_stream():
     q, kv, kp = randn(50, 2, 192).to(DEV), randn(50, 2, 256).to(DEV), randn(50, 64).to(DEV)
