@@ -357,7 +357,8 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
  * out     [Tq, H, 128] (o_st, o_sh); lse [Tq, H] fp32 natural log-sum-exp, or NULL
  * max_q   at least the longest sequence's queries (sizes the grid; a longer sequence
  *         is reported as an index error and skipped). 1 <= H <= 1024; B <= 65535.
- * Rows outside a sequence do not reach its results, whatever they hold. */
+ * Rows outside a sequence do not reach its results, whatever they hold; a row that is
+ * some query's key is finite. */
 int mla_attn_ragged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const void *k_nope, int64_t kn_st,
                     int64_t kn_sh, const void *k_pe, int64_t kp_st, const void *v, int64_t v_st, int64_t v_sh,
                     int64_t Tk, const int32_t *cu_q, const int32_t *cu_k, int B, int max_q, int H, float scale,

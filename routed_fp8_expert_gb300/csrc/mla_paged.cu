@@ -21,14 +21,15 @@ namespace {
 // the key tiles pass through a ring of two (144 KB).
 //
 // One token of 64 heads does 121 flops per byte of cache: the HBM rate bounds it. A tile's
-// MMAs run 1,970 cycles (33 and 49 each, by the shared-memory reads of 64-row operands)
-// of the 3,410 in which HBM delivers one to every SM (2,070 MHz). A ring of two tiles
-// covers that if a tile's way through it stays short: arrival (2,800 cycles from HBM
-// under load), scores, softmax, first products. For the same reason the two products
-// have their issuing warps, and eight warps share a tile's softmax. 256 sequences of
-// 4,246 keys on average: 221 us, 5.8 TB/s of what has to be read and written; 512 new
-// tokens over 7,000 keys, where the tiles come from L2 and the way through the ring
-// bounds it: 956 us, 0.96 PFLOP/s.
+// MMAs run 1,970 cycles (33 and 49 each, the time to read 4 and 6 KB of operands at 128
+// bytes per cycle) of the 3,410 in which HBM delivers one to every SM (2,070 MHz). A ring
+// of two tiles covers that if a tile's way through it stays short: arrival (2,800 cycles
+// from HBM under load), scores, softmax, first products. For the same reason the two
+// products have their issuing warps, and eight warps share a tile's softmax. 256 sequences
+// of 4,246 keys on average: 221 us, 5.8 TB/s of what has to be read and written. Keys that
+// many row tiles read come from L2, and shared memory is the bound: 240 KB that a tile's
+// MMAs read and 80 KB that are written for them take 2,560 cycles of the 2,760 per tile
+// (512 new tokens over 7,000 keys: 956 us, 0.96 PFLOP/s).
 //
 // The work is split evenly by key tiles over the CTAs, whatever the sequences' lengths:
 // the tiles of all (sequence, row tile) items form one line, CTA c takes the c-th part

@@ -19,6 +19,8 @@ namespace {
 // memory, then TMA, which clips rows past T and columns past N) while the next one's
 // products run. W is read as it is stored, K or N contiguous: the descriptor, not a
 // copy, transposes it. Chunks past K, rows past T and columns past N arrive as zeros.
+// 256 tokens of 64 heads, 128 -> 512: 7.1 us, of which the first loads (2 us) and the last
+// stores overlap nothing: 29 MB are 4.3 us of HBM.
 constexpr int kTile = 128;
 constexpr int kChunk = kTile * 128;      // 16 KB: 128 rows of 64 values
 constexpr int kXSlots = 5;
