@@ -1,4 +1,6 @@
 // Absorbed latent attention over the paged cache (mla_attn_paged).
+#include <algorithm>
+
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -29,7 +31,7 @@ namespace {
 // of 4,246 keys on average: 221 us, 5.8 TB/s of what has to be read and written. Keys that
 // many row tiles read come from L2, and shared memory is the bound: 240 KB that a tile's
 // MMAs read and 80 KB that are written for them take 2,560 cycles of the 2,760 per tile
-// (512 new tokens over 7,000 keys: 956 us, 0.96 PFLOP/s).
+// (512 new tokens over 7,000 keys: 950 us, 0.96 PFLOP/s).
 //
 // The work is split evenly by key tiles over the CTAs, whatever the sequences' lengths:
 // the tiles of all (sequence, row tile) items form one line, CTA c takes the c-th part
@@ -59,11 +61,22 @@ constexpr int kTmemS = 256;                      // 2 x 64 columns
 // overflow, and O is rescaled a few times per item instead of once per tile.
 constexpr float kLag = 8.0f;
 constexpr int kNoPage = -0x7fffffff - 1;
-// Fewest key tiles a CTA is given: below it the partial sums cost more than the split gains.
+// Fewest key tiles a CTA is given: below it the partial sums cost more than the split gains
+// (one sequence of 8,000 tokens 19.6 us, with single tiles 23.1). But a CTA with pieces of
+// two items pays for two results and two sets of queries. Where items are short (four tiles
+// on average, kShortItems) and of odd numbers of tiles, single tiles are better: 20 sequences
+// of 50 to 250 tokens 16.6 us against 20.2, of 190 16.4 against 19.6; with even numbers, of
+// 250 17.1 against 16.5, of 128 15.1 against 11.1.
 constexpr int kMinTiles = 2;
+constexpr int kShortItems = 4;
 
 static_assert(kQBytes >= 8192 * 8, "the start-up scan keeps one 8-byte prefix per sequence in the query buffer");
 static_assert(kSmem <= 232448, "shared memory of one CTA");
+static_assert(kSoftWarps == 2 * kGroups, "a softmax warp clears a column group");
+
+struct Seq {
+    int row0, n, ctx;
+};
 
 struct Shared {
     uint64_t pair_full[kPairSlots], pair_empty[kPairSlots];
@@ -78,14 +91,12 @@ struct Shared {
     // the line of key tiles: CTA c's part starts at each * c + min(c, rem)
     int64_t each, lo, hi, start_off;
     int rem, start_b, start_rt;
+    Seq start;
 };
 static_assert(sizeof(Shared) <= 2048, "");
 
 // Queries and visible keys of sequence b. A length or offset outside its buffer is
 // recorded once and leaves the sequence without rows.
-struct Seq {
-    int row0, n, ctx;
-};
 __device__ __forceinline__ Seq read_seq(const PagedArgs &a, int b, bool report) {
     Seq s;
     s.ctx = a.ctx[b];
@@ -121,7 +132,7 @@ struct Walk {
 
     __device__ void start(const PagedArgs &a, const Shared &sh) {
         b = sh.start_b, rt = sh.start_rt, at = sh.lo, hi = sh.hi, off = sh.start_off;
-        s = read_seq(a, b, false);
+        s = sh.start;
         rts = row_tiles(s, a.H);
     }
     __device__ bool next(const PagedArgs &a) {
@@ -220,7 +231,8 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t base = 0;
-    if (tid == 0) sh.start_b = 0, sh.start_rt = 0, sh.start_off = 0;   // a CTA without a part starts nowhere else
+    bool odd = false;
+    if (tid == 0) sh.start_b = 0, sh.start_rt = 0, sh.start_off = 0, sh.start = Seq{0, 0, 0};   // a CTA without a part
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
         Seq s{0, 0, 0};
@@ -247,7 +259,7 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
         }
         const int64_t inc = warp_scan(u, lane);
         if (lane == 31) sh.warp_sum[warp] = inc;
-        __syncthreads();
+        odd |= __syncthreads_or(u & 1);
         int64_t before = base, all = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) before += sh.warp_sum[w];
@@ -257,7 +269,7 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
         base += all;
         __syncthreads();
     }
-    const int64_t most = base / kMinTiles;
+    const int64_t most = odd && base < a.short_line ? base : base / kMinTiles;
     const unsigned parts = most < 1 ? 1u : most < gridDim.x ? static_cast<unsigned>(most) : gridDim.x;
     int64_t each;
     int rem;
@@ -276,13 +288,14 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
             sh.start_b = b;
             sh.start_rt = 0;
             sh.start_off = lo - p;
+            sh.start = read_seq(a, b, false);
         }
     }
     fence_async_smem();   // the prefixes' buffer is filled by TMA next
     __syncthreads();
     if (warp == 0 && lo < hi) {
         // the row tile of that sequence: 32 at a time
-        const Seq s = read_seq(a, sh.start_b, false);
+        const Seq s = sh.start;
         const int rts = row_tiles(s, a.H);
         int64_t off = sh.start_off;
         for (int r0 = 0; r0 < rts; r0 += 32) {
@@ -623,12 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // zero, but zero times a NaN is not
                 const int left = w.keys - kb;
                 if (left < kKeys) {
-                    const uint32_t base = sbase + kOffPairs + (tile & 1) * kGroups * kPairBytes;
-                    const int per = (kKeys - left) * 8;   // 16-byte units per column group
-                    for (int i = tid; i < per * 2 * kGroups; i += kSoftThreads) {
-                        const int g = i / per;
-                        st_shared_v4(base + g * kGroupBytes + left * 128 + (i - g * per) * 16, make_uint4(0, 0, 0, 0));
-                    }
+                    // (a warp per group of 64 columns)
+                    const uint32_t end = sbase + kOffPairs + ((tile & 1) * kSoftWarps + warp + 1) * kGroupBytes;
+                    for (int i = lane; i < (kKeys - left) * 8; i += 32) st_shared_v4(end - 16 - i * 16, make_uint4(0, 0, 0, 0));
                 }
                 tc_fence_before();
                 fence_async_smem();
@@ -673,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 T *out = static_cast<T *>(a.out) + quad * 32 + (lane & 3) * 8;
 #pragma unroll 1
                 for (int c = 0; c < 2 * kRows; c += 32) {
+                    if ((c & 32) >= rows) continue;
                     uint32_t o0[16], o1[16];
                     if (n > 0) {
                         const uint32_t src = tmem + kTmemO + half * 2 * kRows + c + lane_base;
@@ -712,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float *part = a.part_o + static_cast<int64_t>(slot) * kRows * kMlaLatent + quad * 32 + lane;
 #pragma unroll 1
                 for (int c = 0; c < 2 * kRows; c += 32) {
+                    if ((c & 32) >= rows) continue;
                     uint32_t o[32];
                     if (n > 0) {
                         tmem_ld32(tmem + kTmemO + half * 2 * kRows + c + lane_base, o);
@@ -808,6 +820,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
         const int4 j = c < ctas ? a.joins[c] : make_int4(0, 0, 0, 0);
         if (tid < kMaxCtas) s_join[c] = j;
         const int joins = __syncthreads_count(tid < kMaxCtas && j.z > 0);
+        if (joins == 0) return;
         const bool many = j.w - c + 1 > (joins > kFewJoins ? 32 : kAhead);
         rows = many == (tid >= kMaxCtas) ? j.z : 0;
         inc = rows;
@@ -926,7 +939,10 @@ cudaError_t launch_t(const PagedMaps &m, const PagedArgs &a, int grid, cudaStrea
 
 cudaError_t launch_paged(const PagedMaps &m, const PagedArgs &a, bool bf16, int grid, cudaStream_t stream) {
     if (grid > kMaxCtas) return cudaErrorInvalidValue;
-    return bf16 ? launch_t<__nv_bfloat16>(m, a, grid, stream) : launch_t<__half>(m, a, grid, stream);
+    PagedArgs args = a;
+    const int64_t items = std::max<int64_t>(a.B, a.Tq * a.H / kRows);
+    args.short_line = items > 1 ? kShortItems * items : 0;
+    return bf16 ? launch_t<__nv_bfloat16>(m, args, grid, stream) : launch_t<__half>(m, args, grid, stream);
 }
 
 }  // namespace moe

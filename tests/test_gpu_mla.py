@@ -272,6 +272,22 @@ def test_paged_long_context_is_split_and_joined():
     assert torch.equal(o, o2) and torch.equal(lse, lse2)     # the same bits again
 
 
+@pytest.mark.parametrize("H", [16, 40, 64, 100])
+@pytest.mark.parametrize("ctx", [
+    [64] * 7, [65 + 9 * i for i in range(7)], [1 + 11 * i for i in range(20)], [190, 191, 192], [100] * 5 + [700],
+    [3] * 160 + [130], [40] * 90, [0] * 3 + [70, 0, 200],
+])
+def test_paged_short_batches(ctx, H):
+    # one key tile each, two each, mixed, more sequences than processors: every way of cutting
+    n = [1] * len(ctx)
+    q, cache, table, ctx_t = paged_inputs(ctx, n, H, 32, seed=len(ctx) + H, junk=math.nan)
+    o, lse = run_paged(q, cache, table, ctx_t, n)
+    assert error_word() == (_lib.MOE_OK, 0)
+    ro, rl, ob, lb = paged_ref(q, cache, table, ctx_t, n, BF16)
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
+
+
 def test_paged_views_and_strides():
     ctx, n, H = [150, 90], [1, 1], 8
     q, cache, table, ctx_t = paged_inputs(ctx, n, H, 32, seed=11)
