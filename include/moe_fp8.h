@@ -355,7 +355,7 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
  * k_nope  [Tk, H, 128] (kn_st, kn_sh); k_pe [Tk, 64] (kp_st), shared by the heads
  * v       [Tk, H, 128] (v_st, v_sh); k_nope and v may be views of one tensor
  * out     [Tq, H, 128] (o_st, o_sh); lse [Tq, H] fp32 natural log-sum-exp, or NULL
- * max_q   at least the longest sequence's queries (sizes the grid; a longer sequence
+ * max_q   at least the longest sequence's queries (a longer sequence
  *         is reported as an index error and skipped). 1 <= H <= 1024; B <= 65535.
  * Rows outside a sequence do not reach its results, whatever they hold; a row that is
  * some query's key is finite. */

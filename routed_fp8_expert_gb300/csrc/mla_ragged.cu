@@ -44,7 +44,39 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 1024, "");
 
-template <typename T>
+__device__ __forceinline__ bool offsets_ok(const RaggedArgs &a, int64_t q0, int64_t q1, int64_t k0, int64_t k1) {
+    return !(q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk || q1 - q0 > a.max_q);
+}
+__device__ __forceinline__ bool offsets_ok(const RaggedArgs &a, int b) {
+    return offsets_ok(a, a.cu_q[b], a.cu_q[b + 1], a.cu_k[b], a.cu_k[b + 1]);
+}
+
+// The grid has max_q's tiles for every sequence, of which each finds its own, or, where
+// those are kSlotRatio times as many, Tq / 256 + B slots: sequence b's tiles start at slot
+// cu_q[b] / 256 + b, which leaves room for its last, partial one. A CTA without a tile
+// costs 0.7 us of an SM, the search for a slot's sequence as much. 3,000 tokens beside 31
+// prompts of 10: 306 us with max_q's tiles (384 a head), 241 with slots (43); 200 tokens
+// under a bound of 65,536: 81 and 9.6; but nine prompts of 3 to 1,900: 319 (72) and 328
+// (35).
+constexpr int kSlotRatio = 3;
+static_assert(kQRows == 256, "");
+__device__ __forceinline__ int first_slot(const RaggedArgs &a, int b) { return (a.cu_q[b] >> 8) + b; }
+
+// The last sequence that starts at slot x or before (a search by the whole warp).
+__device__ __forceinline__ int sequence_of(const RaggedArgs &a, int x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = a.B;
+    while (n > 1) {
+        const int step = (n + 31) / 32, i = lane * step;
+        const unsigned le = __ballot_sync(0xffffffffu, i < n && first_slot(a, lo + i) <= x);
+        const int k = le ? (31 - __clz(le)) * step : 0;
+        lo += k;
+        n = min(step, n - k);
+    }
+    return lo;
+}
+
+template <typename T, bool SLOTS>
 __global__ void __launch_bounds__(kThreads, 1)
     ragged_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kn,
                        const __grid_constant__ CUtensorMap map_kp, const __grid_constant__ CUtensorMap map_v,
@@ -64,16 +96,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_wait();
     // the longest rows first: they see the most keys
-    const int qt = gridDim.x - 1 - blockIdx.x;
-    const int h = blockIdx.y, b = blockIdx.z;
+    int qt = gridDim.x - 1 - blockIdx.x;
+    const int h = blockIdx.y, b = SLOTS ? sequence_of(a, blockIdx.x) : blockIdx.z;
+    if (SLOTS && h == 0 && threadIdx.x == 0 && blockIdx.x < static_cast<unsigned>(a.B) && !offsets_ok(a, blockIdx.x))
+        record_error(a.err, ERR_BAD_INDEX);   // each of the first B slots looks after one sequence's offsets
     const int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1], kk0 = a.cu_k[b], kk1 = a.cu_k[b + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.Tq || kk0 < 0 || kk1 < kk0 || kk1 > a.Tk || q1 - q0 > a.max_q) {
-        if (threadIdx.x == 0 && qt == 0 && h == 0) record_error(a.err, ERR_BAD_INDEX);
+    if (!offsets_ok(a, q0, q1, kk0, kk1)) {
+        if (!SLOTS && threadIdx.x == 0 && qt == 0 && h == 0) record_error(a.err, ERR_BAD_INDEX);
         return;
     }
     const int nq = static_cast<int>(q1 - q0), nk = static_cast<int>(kk1 - kk0);
+    if (SLOTS) qt = (nq + kQRows - 1) / kQRows - 1 - (static_cast<int>(blockIdx.x) - first_slot(a, b));
     const int r0 = qt * kQRows;
-    if (r0 >= nq) return;
+    if ((SLOTS && qt < 0) || r0 >= nq) return;
     const int rows = min(kQRows, nq - r0);
     const bool two = rows > kTile;
     // keys the CTA's last row sees
@@ -393,22 +428,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) tmem_dealloc<512>(sh.tmem);
 }
 
-template <typename T>
+template <typename T, bool SLOTS>
 cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &kn, const CUtensorMap &kp, const CUtensorMap &v,
-                     const RaggedArgs &a, cudaStream_t stream) {
+                     const RaggedArgs &a, dim3 grid, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(ragged_attn_kernel<T>, kSmem, done);
+    cudaError_t e = allow_smem(ragged_attn_kernel<T, SLOTS>, kSmem, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(ragged_attn_kernel<T>, dim3((a.max_q + kQRows - 1) / kQRows, a.H, a.B), dim3(kThreads), kSmem,
-                      stream, q, kn, kp, v, a);
+    return launch_pdl(ragged_attn_kernel<T, SLOTS>, grid, dim3(kThreads), kSmem, stream, q, kn, kp, v, a);
 }
 
 }  // namespace
 
 cudaError_t launch_ragged(const CUtensorMap &q, const CUtensorMap &k_nope, const CUtensorMap &k_pe,
                           const CUtensorMap &v, const RaggedArgs &a, bool bf16, cudaStream_t stream) {
-    return bf16 ? launch_t<__nv_bfloat16>(q, k_nope, k_pe, v, a, stream)
-                : launch_t<__half>(q, k_nope, k_pe, v, a, stream);
+    const int64_t tiles = (a.max_q + kQRows - 1) / kQRows, slots = a.Tq / kQRows + a.B;
+    if (tiles * a.B >= kSlotRatio * slots) {
+        const dim3 grid(static_cast<unsigned>(slots), a.H);
+        return bf16 ? launch_t<__nv_bfloat16, true>(q, k_nope, k_pe, v, a, grid, stream)
+                    : launch_t<__half, true>(q, k_nope, k_pe, v, a, grid, stream);
+    }
+    const dim3 grid(static_cast<unsigned>(tiles), a.H, a.B);
+    return bf16 ? launch_t<__nv_bfloat16, false>(q, k_nope, k_pe, v, a, grid, stream)
+                : launch_t<__half, false>(q, k_nope, k_pe, v, a, grid, stream);
 }
 
 }  // namespace moe

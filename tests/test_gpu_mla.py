@@ -472,6 +472,33 @@ def test_ragged_bad_offsets_are_reported_and_skipped():
         assert (out == 3.0).all()
 
 
+@pytest.mark.parametrize("nq", [
+    [9], [700, 3, 0, 256, 512, 1, 257], [255, 1, 0, 0, 300] * 8, [i % 4 for i in range(1100)], [0] * 40 + [513] + [0] * 40,
+])
+def test_ragged_long_bound_on_the_queries(nq):
+    # far more room than queries: the grid follows the rows, the results do not change
+    n, H = sum(nq), 2
+    q, kv, kp = randn(n, H, 192, seed=n).to(DEV), randn(n, H, 256, seed=n + 1).to(DEV), randn(n, 64, seed=n + 2).to(DEV)
+    cu = offsets(nq)
+    args = (q, kv[..., :128], kp, kv[..., 128:], cu, cu)
+    o, lse = moe.mla_attn_ragged(*args, 100_000, SCALE, want_lse=True)
+    assert error_word() == (_lib.MOE_OK, 0)
+    ro, rl, ob, lb = ragged_ref(q.cpu(), kv[..., :128].cpu(), kp.cpu(), kv[..., 128:].cpu(), nq, nq, True, BF16)
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
+    o1, lse1 = moe.mla_attn_ragged(*args, max(nq), SCALE, want_lse=True)
+    assert torch.equal(o, o1) and torch.equal(lse, lse1)
+
+
+@pytest.mark.parametrize("bad", [[0, 10, 21], [0, 15, 10], [-3, 10, 20], [0, 300, 20]])
+def test_ragged_bad_offsets_with_a_long_bound(bad):
+    q, kv, kp = randn(20, 1, 192).to(DEV), randn(20, 1, 256).to(DEV), randn(20, 64).to(DEV)
+    cu = torch.tensor(bad, dtype=torch.int32, device=DEV)
+    moe.mla_attn_ragged(q, kv[..., :128], kp, kv[..., 128:], cu, offsets([10, 10]), 100_000, SCALE)
+    assert error_word() == (_lib.MOE_ERR_INDEX, 0x80)
+    assert error_word() == (_lib.MOE_OK, 0)
+
+
 # ------------------------------------------------------------- streams, both forms
 
 def test_absorbed_and_expanded_forms_agree():
