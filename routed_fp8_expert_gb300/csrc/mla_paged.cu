@@ -761,10 +761,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of 64: a warp takes a whole row of up to kAhead parts; rows of more are shared by a
 // CTA, four warps per 128 columns, unless there are enough rows to fill the GPU with
 // a warp each (up to 32 parts: 33 rows' worth of 64 with 6 to 10 parts, 14 -> 9 us).
+// One CTA per SM: with two, 64 registers a thread spilled, and no row count gained from
+// them (33 sequences 42.1 -> 38.0 us, one of 1,000 tokens 16.9 -> 13.5; 256 rows of 38 parts
+// 93.3 -> 95.6).
 constexpr int kJoinThreads = 512;
 constexpr int kMaxCtas = 256;
-constexpr int kFewJoins = 8;
-constexpr int kAhead = 8;    // parts whose sums are on their way together
+constexpr int kFewJoins = 8, kFewParts = 8;
+constexpr int kAhead = 16;   // parts whose sums are on their way together
 
 // Sum of parts [s0, s1) of a row for four columns, relative to their largest reference
 // maximum M, and the sum L of their exponentials (s1 - s0 <= 64).
@@ -803,15 +806,15 @@ __device__ __forceinline__ float4 join_parts(const PagedArgs &a, SlotOf slot_of,
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const PagedArgs a, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, 1) paged_join_kernel(const PagedArgs a, int ctas) {
     // rows before join c, of the joins of few parts and of many
     __shared__ int s_rows[2][kMaxCtas + 1];
     __shared__ int s_sum[2][kMaxCtas / 32];
     __shared__ int4 s_join[kMaxCtas];
-    __shared__ float4 s_acc[3][4][32];
-    __shared__ float2 s_ml[4];
+    __shared__ float4 s_acc[kJoinThreads / 32 - 2][32];
+    __shared__ float2 s_ml[8];
     pdl_trigger();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = warp & 3, grp = warp >> 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     int rows = 0, inc = 0;
     static_assert(kJoinThreads == 2 * kMaxCtas, "thread = (kind, join)");
@@ -821,7 +824,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
         if (tid < kMaxCtas) s_join[c] = j;
         const int joins = __syncthreads_count(tid < kMaxCtas && j.z > 0);
         if (joins == 0) return;
-        const bool many = j.w - c + 1 > (joins > kFewJoins ? 32 : kAhead);
+        const bool many = j.w - c + 1 > (joins > kFewJoins ? 32 : kFewParts);
         rows = many == (tid >= kMaxCtas) ? j.z : 0;
         inc = rows;
 #pragma unroll
@@ -839,7 +842,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
         if (c == 0) s_rows[kind][0] = 0;
     }
     __syncthreads();
-    const int col = slice * 128 + lane * 4;
     auto find = [&](int kind, int i) {   // the join with s_rows[c] <= i < s_rows[c + 1]
         int lo = 0, hi = kMaxCtas;
         while (hi - lo > 1) {
@@ -895,29 +897,35 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
 #pragma unroll
         for (int k = 0; k < 4; ++k) store(j, r, k * 128 + lane * 4, acc[k], M, L);
     }
-    for (int i = blockIdx.x; i < s_rows[1][kMaxCtas]; i += gridDim.x) {
-        const int c = find(1, i), r = i - s_rows[1][c];
+    // Rows of many parts: a CTA takes all of a row's columns in four slices, the parts in
+    // four shares, or, if there are CTAs enough, half of the columns and eight shares (one
+    // sequence of 20,000 tokens, 152 parts: 20.1 us, with four shares 25.0; three of 8,000,
+    // 192 rows: 24.8 and 24.1).
+    const int half = 2 * s_rows[1][kMaxCtas] <= static_cast<int>(gridDim.x) ? 1 : 0;
+    const int slices = 4 >> half, shares = 4 << half, slice = warp & (slices - 1), grp = warp >> (2 - half);
+    for (int i = blockIdx.x; i < s_rows[1][kMaxCtas] << half; i += gridDim.x) {
+        const int row = i >> half, col = ((i & half) * 2 + slice) * 128 + lane * 4;
+        const int c = find(1, row), r = row - s_rows[1][c];
         const int4 j = s_join[c];
-        const int parts = j.w - c + 1, per = (parts + 3) / 4;
+        const int parts = j.w - c + 1, per = (parts + shares - 1) >> (2 + half);
         auto slot_of = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * kRows + r; };
         float M, L;
         float4 acc = join_parts(a, slot_of, min(parts, grp * per), min(parts, (grp + 1) * per), col, M, L);
         __syncthreads();   // the last row's sums have been read
-        if (grp > 0) s_acc[grp - 1][slice][lane] = acc;
+        if (grp > 0) s_acc[warp - slices][lane] = acc;
         if (slice == 0 && lane == 0) s_ml[grp] = make_float2(M, L);
         __syncthreads();
         if (grp == 0) {
             float m = M;
-#pragma unroll
-            for (int g = 1; g < 4; ++g) m = fmaxf(m, s_ml[g].x);
+            for (int g = 1; g < shares; ++g) m = fmaxf(m, s_ml[g].x);
             float f = M == -INFINITY ? 0.f : ex2(M - m);
             L *= f;
             acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-#pragma unroll
-            for (int g = 1; g < 4; ++g) {
+#pragma unroll 1
+            for (int g = 1; g < shares; ++g) {
                 f = s_ml[g].x == -INFINITY ? 0.f : ex2(s_ml[g].x - m);
                 L += f * s_ml[g].y;
-                const float4 x = s_acc[g - 1][slice][lane];
+                const float4 x = s_acc[(g - 1) * slices + slice][lane];
                 acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
             }
             store(j, r, col, acc, m, L);
@@ -932,7 +940,7 @@ cudaError_t launch_t(const PagedMaps &m, const PagedArgs &a, int grid, cudaStrea
     if (e != cudaSuccess) return e;
     e = launch_pdl(paged_attn_kernel<T>, dim3(grid), dim3(kThreads), kSmem, stream, m, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_join_kernel<T>, dim3(2 * grid), dim3(kJoinThreads), 0, stream, a, grid);
+    return launch_pdl(paged_join_kernel<T>, dim3(grid), dim3(kJoinThreads), 0, stream, a, grid);
 }
 
 }  // namespace
