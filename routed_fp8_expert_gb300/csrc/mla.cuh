@@ -365,7 +365,7 @@ struct PagedArgs {
     int q_box;                // heads of one query load
     int B, H;
     float scale_log2;         // scale * log2(e)
-    int64_t short_line;       // below so many key tiles in all the items are short (launch_paged)
+    int few_joins;            // joins whose rows are few (launch_paged)
     float *part_o;            // [2 * grid][64][512]
     float2 *part_ml;          // [2 * grid][64]
     int4 *joins;              // [grid]

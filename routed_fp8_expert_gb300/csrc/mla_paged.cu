@@ -61,14 +61,12 @@ constexpr int kTmemS = 256;                      // 2 x 64 columns
 // overflow, and O is rescaled a few times per item instead of once per tile.
 constexpr float kLag = 8.0f;
 constexpr int kNoPage = -0x7fffffff - 1;
-// Fewest key tiles a CTA is given: below it the partial sums cost more than the split gains
-// (one sequence of 8,000 tokens 19.6 us, with single tiles 23.1). But a CTA with pieces of
-// two items pays for two results and two sets of queries. Where items are short (four tiles
-// on average, kShortItems) and of odd numbers of tiles, single tiles are better: 20 sequences
-// of 50 to 250 tokens 16.6 us against 20.2, of 190 16.4 against 19.6; with even numbers, of
-// 250 17.1 against 16.5, of 128 15.1 against 11.1.
-constexpr int kMinTiles = 2;
-constexpr int kShortItems = 4;
+// Fewest key tiles a CTA is given: one, unless every item has an even number of them. Then
+// two make half as many partial sums, and still no CTA has pieces of two items, which would
+// cost it two results and two sets of queries (two sequences of 4,000 tokens, 63 tiles:
+// 19.3 us with two tiles, 16.4 with one; 60 of 128: 12.6 and 16.4; 8 of 1,000: 17.4 and
+// 18.7; one of 1,000: 13.7 and 13.1).
+constexpr int kEvenTiles = 2;
 
 static_assert(kQBytes >= 8192 * 8, "the start-up scan keeps one 8-byte prefix per sequence in the query buffer");
 static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -269,7 +267,7 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
         base += all;
         __syncthreads();
     }
-    const int64_t most = odd && base < a.short_line ? base : base / kMinTiles;
+    const int64_t most = odd ? base : base / kEvenTiles;
     const unsigned parts = most < 1 ? 1u : most < gridDim.x ? static_cast<unsigned>(most) : gridDim.x;
     int64_t each;
     int rem;
@@ -757,16 +755,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   M = max m_s,  O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s
 // over the item's parts in order. joins[c] = (the sequence's first query, first row of
 // the tile, rows, last CTA) of the item whose first part CTA c holds (rows 0: none).
-// A large batch has two parts of each of 10,000 rows, a single long sequence 60 parts
-// of 64: a warp takes a whole row of up to kAhead parts; rows of more are shared by a
-// CTA, four warps per 128 columns, unless there are enough rows to fill the GPU with
-// a warp each (up to 32 parts: 33 rows' worth of 64 with 6 to 10 parts, 14 -> 9 us).
+// A large batch has two parts of each of 10,000 rows, a single long sequence up to 150 of
+// each of 64. More than kFewRows rows: a warp takes a whole row of up to 32 parts (33
+// sequences' 64 rows of 6 to 10 parts 14 -> 9 us). Fewer, or rows of more parts: a CTA takes
+// a row, or half of one. (128 rows of 16 parts 13.2 us a call, with a warp each 16.8; 320
+// rows of 11 parts 18.4 and 16.3, of 25 parts 19.6 and 21.4. Both kinds in one call cost
+// the sum: 12 sequences of 16 heads and 5 to 11 parts 16.5, either kind 15.)
 // One CTA per SM: with two, 64 registers a thread spilled, and no row count gained from
 // them (33 sequences 42.1 -> 38.0 us, one of 1,000 tokens 16.9 -> 13.5; 256 rows of 38 parts
 // 93.3 -> 95.6).
 constexpr int kJoinThreads = 512;
 constexpr int kMaxCtas = 256;
-constexpr int kFewJoins = 8, kFewParts = 8;
+constexpr int kFewRows = 300;
 constexpr int kAhead = 16;   // parts whose sums are on their way together
 
 // Sum of parts [s0, s1) of a row for four columns, relative to their largest reference
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) paged_join_kernel(const Paged
         if (tid < kMaxCtas) s_join[c] = j;
         const int joins = __syncthreads_count(tid < kMaxCtas && j.z > 0);
         if (joins == 0) return;
-        const bool many = j.w - c + 1 > (joins > kFewJoins ? 32 : kFewParts);
+        const bool many = j.w - c + 1 > (joins > a.few_joins ? 32 : 0);
         rows = many == (tid >= kMaxCtas) ? j.z : 0;
         inc = rows;
 #pragma unroll
@@ -948,8 +948,8 @@ cudaError_t launch_t(const PagedMaps &m, const PagedArgs &a, int grid, cudaStrea
 cudaError_t launch_paged(const PagedMaps &m, const PagedArgs &a, bool bf16, int grid, cudaStream_t stream) {
     if (grid > kMaxCtas) return cudaErrorInvalidValue;
     PagedArgs args = a;
-    const int64_t items = std::max<int64_t>(a.B, a.Tq * a.H / kRows);
-    args.short_line = items > 1 ? kShortItems * items : 0;
+    const int64_t item_rows = std::min<int64_t>(kRows, (a.Tq * a.H + a.B - 1) / a.B);
+    args.few_joins = static_cast<int>(kFewRows / std::max<int64_t>(item_rows, 1));
     return bf16 ? launch_t<__nv_bfloat16>(m, args, grid, stream) : launch_t<__half>(m, args, grid, stream);
 }
 
