@@ -761,16 +761,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 // a row, or half of one. (128 rows of 16 parts 13.2 us a call, with a warp each 16.8; 320
 // rows of 11 parts 18.4 and 16.3, of 25 parts 19.6 and 21.4. Both kinds in one call cost
 // the sum: 12 sequences of 16 heads and 5 to 11 parts 16.5, either kind 15.)
-// One CTA per SM: with two, 64 registers a thread spilled, and no row count gained from
-// them (33 sequences 42.1 -> 38.0 us, one of 1,000 tokens 16.9 -> 13.5; 256 rows of 38 parts
-// 93.3 -> 95.6).
-constexpr int kJoinThreads = 512;
+// Two CTAs of 256 threads per SM with 128 registers each: with 512 threads the 64 registers
+// spilled (33 sequences 42.1 -> 38.0 us, one of 1,000 tokens 16.9 -> 13.5); one CTA of 512
+// had to take 150 to 300 rows in two turns (4 x 1,000 tokens 16.6 -> 14.9 us).
+constexpr int kJoinThreads = 256;
 constexpr int kMaxCtas = 256;
 constexpr int kFewRows = 300;
 constexpr int kAhead = 16;   // parts whose sums are on their way together
 
 // Sum of parts [s0, s1) of a row for four columns, relative to their largest reference
-// maximum M, and the sum L of their exponentials (s1 - s0 <= 64).
+// maximum M, and the sum L of their exponentials (s1 - s0 <= 128).
 template <typename SlotOf>
 __device__ __forceinline__ float4 join_parts(const PagedArgs &a, SlotOf slot_of, int s0, int s1, int col, float &M, float &L) {
     const int lane = threadIdx.x & 31;
@@ -779,23 +779,31 @@ __device__ __forceinline__ float4 join_parts(const PagedArgs &a, SlotOf slot_of,
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
         if (s0 + k < s1) v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot_of(s0 + k) * kMlaLatent + col));
-    const float2 none = make_float2(-INFINITY, 0.f);
-    const float2 m0 = s0 + lane < s1 ? a.part_ml[slot_of(s0 + lane)] : none;
-    const float2 m1 = s0 + 32 + lane < s1 ? a.part_ml[slot_of(s0 + 32 + lane)] : none;
-    M = fmaxf(m0.x, m1.x);
+    static_assert(kMaxCtas <= 2 * 128, "two shares of an item's parts");
+    float2 ml[4];
+    M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        ml[k] = s0 + 32 * k + lane < s1 ? a.part_ml[slot_of(s0 + 32 * k + lane)] : make_float2(-INFINITY, 0.f);
+        M = fmaxf(M, ml[k].x);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    // a part without visible keys has weight zero and sums of zero
-    const float w0 = m0.x == -INFINITY ? 0.f : ex2(m0.x - M), w1 = m1.x == -INFINITY ? 0.f : ex2(m1.x - M);
-    L = w0 * m0.y + w1 * m1.y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        // a part without visible keys has weight zero and sums of zero
+        ml[k].x = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
+        L += ml[k].x * ml[k].y;
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 < s1 - s0; k0 += kAhead) {
+        const float w = k0 < 32 ? ml[0].x : k0 < 64 ? ml[1].x : k0 < 96 ? ml[2].x : ml[3].x;   // (kAhead divides 32)
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             if (s0 + k0 + k < s1) {
-                const float f = __shfl_sync(0xffffffffu, k0 < 32 ? w0 : w1, (k0 + k) & 31);
+                const float f = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
                 acc.x += f * v[k].x, acc.y += f * v[k].y, acc.z += f * v[k].z, acc.w += f * v[k].w;
                 if (s0 + k0 + kAhead + k < s1)
                     v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot_of(s0 + k0 + kAhead + k) * kMlaLatent + col));
@@ -806,40 +814,34 @@ __device__ __forceinline__ float4 join_parts(const PagedArgs &a, SlotOf slot_of,
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads, 1) paged_join_kernel(const PagedArgs a, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const PagedArgs a, int ctas) {
     // rows before join c, of the joins of few parts and of many
     __shared__ int s_rows[2][kMaxCtas + 1];
-    __shared__ int s_sum[2][kMaxCtas / 32];
+    __shared__ unsigned s_sum[kMaxCtas / 32];
     __shared__ int4 s_join[kMaxCtas];
-    __shared__ float4 s_acc[kJoinThreads / 32 - 2][32];
-    __shared__ float2 s_ml[8];
+    __shared__ float4 s_acc[kJoinThreads / 32 - 1][32];
+    __shared__ float2 s_ml[kJoinThreads / 32];
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
-    int rows = 0, inc = 0;
-    static_assert(kJoinThreads == 2 * kMaxCtas, "thread = (kind, join)");
+    static_assert(kJoinThreads == kMaxCtas && kMaxCtas * kRows < 1 << 16, "a thread's join; both counts in one word");
     {
-        const int c = tid % kMaxCtas;
-        const int4 j = c < ctas ? a.joins[c] : make_int4(0, 0, 0, 0);
-        if (tid < kMaxCtas) s_join[c] = j;
-        const int joins = __syncthreads_count(tid < kMaxCtas && j.z > 0);
+        const int4 j = tid < ctas ? a.joins[tid] : make_int4(0, 0, 0, 0);
+        s_join[tid] = j;
+        const int joins = __syncthreads_count(j.z > 0);
         if (joins == 0) return;
-        const bool many = j.w - c + 1 > (joins > a.few_joins ? 32 : 0);
-        rows = many == (tid >= kMaxCtas) ? j.z : 0;
-        inc = rows;
+        const bool many = j.w - tid + 1 > (joins > a.few_joins ? 32 : 0);
+        unsigned inc = static_cast<unsigned>(j.z) << (many ? 16 : 0);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, inc, o);
+            const unsigned u = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += u;
         }
-        if (lane == 31) s_sum[tid / kMaxCtas][c / 32] = inc;
-    }
-    __syncthreads();
-    {
-        const int kind = tid / kMaxCtas, c = tid % kMaxCtas;
-        for (int i = 0; i < c / 32; ++i) inc += s_sum[kind][i];
-        s_rows[kind][c + 1] = inc;
-        if (c == 0) s_rows[kind][0] = 0;
+        if (lane == 31) s_sum[warp] = inc;
+        __syncthreads();
+        for (int i = 0; i < warp; ++i) inc += s_sum[i];
+        s_rows[0][tid + 1] = inc & 0xffff, s_rows[1][tid + 1] = inc >> 16;
+        if (tid == 0) s_rows[0][0] = s_rows[1][0] = 0;
     }
     __syncthreads();
     auto find = [&](int kind, int i) {   // the join with s_rows[c] <= i < s_rows[c + 1]
@@ -898,16 +900,17 @@ __global__ void __launch_bounds__(kJoinThreads, 1) paged_join_kernel(const Paged
         for (int k = 0; k < 4; ++k) store(j, r, k * 128 + lane * 4, acc[k], M, L);
     }
     // Rows of many parts: a CTA takes all of a row's columns in four slices, the parts in
-    // four shares, or, if there are CTAs enough, half of the columns and eight shares (one
-    // sequence of 20,000 tokens, 152 parts: 20.1 us, with four shares 25.0; three of 8,000,
-    // 192 rows: 24.8 and 24.1).
-    const int half = 2 * s_rows[1][kMaxCtas] <= static_cast<int>(gridDim.x) ? 1 : 0;
-    const int slices = 4 >> half, shares = 4 << half, slice = warp & (slices - 1), grp = warp >> (2 - half);
-    for (int i = blockIdx.x; i < s_rows[1][kMaxCtas] << half; i += gridDim.x) {
-        const int row = i >> half, col = ((i & half) * 2 + slice) * 128 + lane * 4;
+    // two shares, or, if there are CTAs enough, half of the columns and four shares, or a
+    // quarter and eight (one sequence of 20,000 tokens, 152 parts: 20.1 us with eight shares,
+    // 25.0 with four).
+    const int rows = s_rows[1][kMaxCtas], ctas_free = gridDim.x;
+    const int split = 4 * rows <= ctas_free ? 2 : 2 * rows <= ctas_free ? 1 : 0;
+    const int slices = 4 >> split, shares = 2 << split, slice = warp & (slices - 1), grp = warp >> (2 - split);
+    for (int i = blockIdx.x; i < rows << split; i += gridDim.x) {
+        const int row = i >> split, col = ((i & ((1 << split) - 1)) * slices + slice) * 128 + lane * 4;
         const int c = find(1, row), r = row - s_rows[1][c];
         const int4 j = s_join[c];
-        const int parts = j.w - c + 1, per = (parts + shares - 1) >> (2 + half);
+        const int parts = j.w - c + 1, per = (parts + shares - 1) >> (1 + split);
         auto slot_of = [&](int s) { return static_cast<int64_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * kRows + r; };
         float M, L;
         float4 acc = join_parts(a, slot_of, min(parts, grp * per), min(parts, (grp + 1) * per), col, M, L);
@@ -940,7 +943,7 @@ cudaError_t launch_t(const PagedMaps &m, const PagedArgs &a, int grid, cudaStrea
     if (e != cudaSuccess) return e;
     e = launch_pdl(paged_attn_kernel<T>, dim3(grid), dim3(kThreads), kSmem, stream, m, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_join_kernel<T>, dim3(grid), dim3(kJoinThreads), 0, stream, a, grid);
+    return launch_pdl(paged_join_kernel<T>, dim3(2 * grid), dim3(kJoinThreads), 0, stream, a, grid);
 }
 
 }  // namespace
