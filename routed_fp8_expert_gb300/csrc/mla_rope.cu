@@ -8,7 +8,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+// Tokens of few heads, kFewVecs 16-byte units of queries at most, take CTAs of 128 threads
+// when they outnumber the eight of 256 that an SM holds: 8192 tokens of 16 heads 16.5 -> 11.7
+// us, of 32 (half layout) 20.8 -> 15.3; but 1024 of 16 3.5 -> 4.1.
+constexpr int kFewVecs = 128;
 
 // One CTA per token. With f_i the pair's frequency in turns per position,
 //   (a, b) -> amplitude * (a cos - b sin, b cos + a sin),  angle = 2 pi frac(pos * f_i).
@@ -25,10 +28,10 @@ constexpr int kRopeThreads = 256;
 // dimension when it is known at compile time (64, else 0), the divisions by a head's
 // vectors are shifts (34.3 us without either). 8192 tokens of 64 heads: 31.1 us, 4.9 TB/s
 // (27.3 us for a dense copy of the queries' 134 MB alone).
-template <typename T, bool HALF, int DIM>
-__global__ void __launch_bounds__(kRopeThreads, 8) rope_append_kernel(const RopeArgs a) {
+template <typename T, bool HALF, int DIM, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) rope_append_kernel(const RopeArgs a) {
     __shared__ __align__(16) float2 s_cs[128];
-    __shared__ float s_part[kRopeThreads / 32];
+    __shared__ float s_part[THREADS / 32];
     pdl_trigger();
     pdl_wait();
     const int64_t t = blockIdx.x;
@@ -109,11 +112,11 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_append_kernel(const Rope
     Pair early[kEarly];
 #pragma unroll
     for (int k = 0; k < kEarly; ++k) {
-        const unsigned i = tid + k * kRopeThreads;
+        const unsigned i = tid + k * THREADS;
         if (i < items) early[k] = fetch(q + i / nvec * a.q_sh, i % nvec);
     }
     // the rotary key: the last threads, which hold no part of a 512-column latent
-    const unsigned kvec = kRopeThreads - 1 - tid;
+    const unsigned kvec = THREADS - 1 - tid;
     Pair key;
     if (kv && kvec < nvec) key = fetch(kv + a.latent, kvec);
     __syncthreads();
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_append_kernel(const Rope
             if (a.gamma) {
                 float ss = 0.f;
 #pragma unroll
-                for (int i = 0; i < kRopeThreads / 32; ++i) ss += i < c_warps ? s_part[i] : 0.f;
+                for (int i = 0; i < THREADS / 32; ++i) ss += i < c_warps ? s_part[i] : 0.f;
                 const float inv = 1.0f / sqrtf(ss / static_cast<float>(a.latent) + a.eps);
                 const uint4 gv = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.gamma) + tid * 8);
                 const uint32_t *g = reinterpret_cast<const uint32_t *>(&gv), *w = reinterpret_cast<const uint32_t *>(&cv);
@@ -160,10 +163,10 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_append_kernel(const Rope
         T *qo = static_cast<T *>(a.q_out) + t * a.qo_st;
 #pragma unroll
         for (int k = 0; k < kEarly; ++k) {
-            const unsigned i = tid + k * kRopeThreads;
+            const unsigned i = tid + k * THREADS;
             if (i < items) rotate(early[k], qo + i / nvec * a.qo_sh, nullptr, i % nvec);
         }
-        for (unsigned i = tid + kEarly * kRopeThreads; i < items; i += kRopeThreads)
+        for (unsigned i = tid + kEarly * THREADS; i < items; i += THREADS)
             rotate(fetch(q + i / nvec * a.q_sh, i % nvec), qo + i / nvec * a.qo_sh, nullptr, i % nvec);
     }
 }
@@ -172,9 +175,14 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_append_kernel(const Rope
 
 template <typename T>
 static cudaError_t launch_t(const RopeArgs &a, cudaStream_t stream) {
-    auto kernel = a.dim == 64 ? (a.layout ? rope_append_kernel<T, true, 64> : rope_append_kernel<T, false, 64>)
-                              : (a.layout ? rope_append_kernel<T, true, 0> : rope_append_kernel<T, false, 0>);
-    return launch_pdl(kernel, dim3(a.T), dim3(kRopeThreads), 0, stream, a);
+    const int vecs = a.q ? a.H * (a.layout ? a.dim / 16 : a.dim / 8) : 0;   // 16-byte units of a token's queries
+    if (a.dim == 64 && vecs <= kFewVecs && a.latent <= 8 * 128 && a.T > 8 * num_sms()) {
+        auto kernel = a.layout ? rope_append_kernel<T, true, 64, 128> : rope_append_kernel<T, false, 64, 128>;
+        return launch_pdl(kernel, dim3(a.T), dim3(128), 0, stream, a);
+    }
+    auto kernel = a.dim == 64 ? (a.layout ? rope_append_kernel<T, true, 64, 256> : rope_append_kernel<T, false, 64, 256>)
+                              : (a.layout ? rope_append_kernel<T, true, 0, 256> : rope_append_kernel<T, false, 0, 256>);
+    return launch_pdl(kernel, dim3(a.T), dim3(256), 0, stream, a);
 }
 
 cudaError_t launch_rope(const RopeArgs &a, bool bf16, cudaStream_t stream) {

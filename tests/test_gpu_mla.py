@@ -170,6 +170,28 @@ def test_rope_of_a_strided_multi_layer_cache():
     assert (big[:, 0] == 0).all() and (big[:, 2] == 0).all() and (flat[:7] == 0).all() and (flat[27:] == 0).all()
 
 
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("H,latent", [(1, 512), (16, 512), (32, 1024), (5, 1032), (0, 512)])
+def test_rope_long_calls_equal_short_ones(H, latent, layout):
+    # many tokens of few heads are launched in another shape: the same bits token by token
+    T = 3001
+    plan = moe.rope_plan(64, 50000.0, 32.0, layout=layout, device=DEV)
+    q, kv = randn(T, H, 64, seed=1).to(DEV) if H else None, randn(T, latent + 64, seed=2).to(DEV)
+    gamma = randn(latent, seed=3).to(DEV)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV) * 41
+    slots = torch.arange(T, dtype=torch.int32, device=DEV)
+    cache = torch.zeros(2, 47, 64, latent + 64, dtype=BF16, device=DEV)
+    rows = torch.zeros(2, T, latent + 64, dtype=BF16, device=DEV)
+    whole, _ = moe.mla_rope_append(q, kv, pos, plan, gamma=gamma, cache=cache[0], slots=slots, kv_out=rows[0])
+    for i in range(0, T, 500):
+        c = slice(i, min(T, i + 500))
+        part, _ = moe.mla_rope_append(q[c] if H else None, kv[c], pos[c], plan, gamma=gamma, cache=cache[1],
+                                      slots=slots[c], kv_out=rows[1, c])
+        assert not H or torch.equal(whole[c], part)
+    assert torch.equal(cache[0], cache[1]) and torch.equal(rows[0], rows[1]) and (rows[0] != 0).any(1).all()
+    assert error_word() == (_lib.MOE_OK, 0)
+
+
 # ----------------------------------------------------------------------- paged
 
 def paged_inputs(ctx, n, H, page, seed=0, dtype=BF16, std=1.0, junk=None, extra_cols=3):
