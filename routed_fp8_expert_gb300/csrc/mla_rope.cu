@@ -8,11 +8,6 @@ namespace moe {
 
 namespace {
 
-// Tokens of few heads, kFewVecs 16-byte units of queries at most, take CTAs of 128 threads
-// when they outnumber the eight of 256 that an SM holds: 8192 tokens of 16 heads 16.5 -> 11.7
-// us, of 32 (half layout) 20.8 -> 15.3; but 1024 of 16 3.5 -> 4.1.
-constexpr int kFewVecs = 128;
-
 // One CTA per token. With f_i the pair's frequency in turns per position,
 //   (a, b) -> amplitude * (a cos - b sin, b cos + a sin),  angle = 2 pi frac(pos * f_i).
 // The frequency is a 64-bit fixed-point fraction of a turn, so pos * f_i wraps modulo
@@ -23,11 +18,13 @@ constexpr int kFewVecs = 128;
 // fp32, rounded once when stored.
 //
 // A prompt is bound by memory, and nearly as much by the issue rate. 32 bytes per thread
-// are on their way before the angles are known, and 32 registers keep eight CTAs on an SM
-// (six: 33.5 us); what only the key's warps need is theirs alone, and with DIM, the rotary
-// dimension when it is known at compile time (64, else 0), the divisions by a head's
-// vectors are shifts (34.3 us without either). 8192 tokens of 64 heads: 31.1 us, 4.9 TB/s
-// (27.3 us for a dense copy of the queries' 134 MB alone).
+// are on their way before the angles are known; what only the key's warps need is theirs
+// alone, and with DIM, the rotary dimension when it is known at compile time (64, else 0),
+// the divisions by a head's vectors are shifts. 32 registers and CTAs of 128 threads keep
+// sixteen tokens on an SM: 8192 tokens of 64 heads 28.3 us, 5.4 TB/s (with 256 threads
+// 31.3, without the two before 34.3; 27.3 for a dense copy of the queries' 134 MB alone),
+// of 16 heads 11.7 (16.5). Where an SM has no more than eight tokens, 256 threads have
+// each done sooner (1024 tokens of 16 heads 3.5 us, with 128 threads 4.1).
 template <typename T, bool HALF, int DIM, int THREADS>
 __global__ void __launch_bounds__(THREADS, 2048 / THREADS) rope_append_kernel(const RopeArgs a) {
     __shared__ __align__(16) float2 s_cs[128];
@@ -175,8 +172,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) rope_append_kernel(co
 
 template <typename T>
 static cudaError_t launch_t(const RopeArgs &a, cudaStream_t stream) {
-    const int vecs = a.q ? a.H * (a.layout ? a.dim / 16 : a.dim / 8) : 0;   // 16-byte units of a token's queries
-    if (a.dim == 64 && vecs <= kFewVecs && a.latent <= 8 * 128 && a.T > 8 * num_sms()) {
+    if (a.dim == 64 && a.latent <= 8 * 128 && a.T > 8 * num_sms()) {
         auto kernel = a.layout ? rope_append_kernel<T, true, 64, 128> : rope_append_kernel<T, false, 64, 128>;
         return launch_pdl(kernel, dim3(a.T), dim3(128), 0, stream, a);
     }
