@@ -259,7 +259,8 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
         if (lane == 31) sh.warp_sum[warp] = inc;
         odd |= __syncthreads_or(u & 1);
         int64_t before = base, all = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
+#pragma unroll 1
+        for (int w = 0; w < min(kThreads, a.B - b0 + 31) / 32; ++w) {   // (short code: it runs once)
             if (w < warp) before += sh.warp_sum[w];
             all += sh.warp_sum[w];
         }
@@ -291,10 +292,10 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
     }
     fence_async_smem();   // the prefixes' buffer is filled by TMA next
     __syncthreads();
-    if (warp == 0 && lo < hi) {
+    const Seq s = sh.start;
+    const int rts = row_tiles(s, a.H);
+    if (warp == 0 && rts > 1) {
         // the row tile of that sequence: 32 at a time
-        const Seq s = sh.start;
-        const int rts = row_tiles(s, a.H);
         int64_t off = sh.start_off;
         for (int r0 = 0; r0 < rts; r0 += 32) {
             const int64_t u = r0 + lane < rts ? units_of(tile_keys(s, r0 + lane, a.H)) : 0;
