@@ -351,6 +351,23 @@ struct RopeArgs {
     unsigned int *err;
 };
 
+// Division of 0 <= x < 2^31 by a divisor known on the host, in three instructions instead of
+// twenty (Granlund and Montgomery, 1994): with 2^s >= d, m = floor(2^32 (2^s - d) / d) + 1,
+// x / d = (hi(x m) + x) >> s.
+struct Divisor {
+    uint32_t mul, shift;
+    Divisor() = default;
+    explicit Divisor(uint32_t d) : shift(0) {
+        while ((uint64_t{1} << shift) < d) ++shift;
+        mul = static_cast<uint32_t>((((uint64_t{1} << shift) - d) << 32) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int div(int x) const {
+        return static_cast<int>((__umulhi(static_cast<uint32_t>(x), mul) + static_cast<uint32_t>(x)) >> shift);
+    }
+#endif
+};
+
 struct PagedArgs {
     int64_t Tq;
     const int32_t *table;     // [B, table_st]
@@ -364,6 +381,7 @@ struct PagedArgs {
     int max_pages, page_size, box_rows;
     int q_box;                // heads of one query load
     int B, H;
+    Divisor by_H, by_page;    // (launch_paged)
     float scale_log2;         // scale * log2(e)
     int few_joins;            // joins whose rows are few (launch_paged)
     float *part_o;            // [2 * grid][64][512]

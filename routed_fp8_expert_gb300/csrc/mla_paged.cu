@@ -114,9 +114,9 @@ __device__ __forceinline__ int row_tiles(const Seq &s, int H) { return (s.n * H 
 
 // Keys that the last row of a row tile sees, and the key tiles that cover them (at
 // least one unit of work, so that rows without keys get their zeros).
-__device__ __forceinline__ int tile_keys(const Seq &s, int rt, int H) {
-    const int last = min((rt + 1) * kRows, s.n * H) - 1;
-    return max(0, s.ctx - s.n + last / H + 1);
+__device__ __forceinline__ int tile_keys(const PagedArgs &a, const Seq &s, int rt) {
+    const int last = min((rt + 1) * kRows, s.n * a.H) - 1;
+    return max(0, s.ctx - s.n + a.by_H.div(last) + 1);
 }
 __device__ __forceinline__ int units_of(int keys) { return keys <= kKeys ? 1 : (keys - 1) / kKeys + 1; }
 
@@ -144,7 +144,7 @@ struct Walk {
                 rts = row_tiles(s, a.H);
                 continue;
             }
-            keys = tile_keys(s, rt, a.H);
+            keys = tile_keys(a, s, rt);
             const int u = units_of(keys);
             if (off >= u) {
                 off -= u;
@@ -190,9 +190,10 @@ struct Cursor {
             } while (n == 0);
             j = 0;
             key = w.k0 * kKeys;
-            at = key % a.page_size;
+            const int first = a.by_page.div(key);
+            at = key - first * a.page_size;
             end = min(w.keys, w.k1 * kKeys);
-            tab = a.table + static_cast<int64_t>(w.b) * a.table_st + key / a.page_size;
+            tab = a.table + static_cast<int64_t>(w.b) * a.table_st + first;
         }
         ++j;
 #pragma unroll
@@ -239,7 +240,7 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
         const int rts = row_tiles(s, a.H);
         // few row tiles: one thread per sequence; many: the warp takes them together
         if (rts <= 8)
-            for (int r = 0; r < rts; ++r) u += units_of(tile_keys(s, r, a.H));
+            for (int r = 0; r < rts; ++r) u += units_of(tile_keys(a, s, r));
         unsigned many = __ballot_sync(0xffffffffu, rts > 8);
         while (many) {
             const int src = __ffs(many) - 1;
@@ -250,7 +251,7 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
             o.ctx = __shfl_sync(0xffffffffu, s.ctx, src);
             const int orts = __shfl_sync(0xffffffffu, rts, src);
             int64_t v = 0;
-            for (int r = lane; r < orts; r += 32) v += units_of(tile_keys(o, r, a.H));
+            for (int r = lane; r < orts; r += 32) v += units_of(tile_keys(a, o, r));
 #pragma unroll
             for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
             if (lane == src) u = v;
@@ -272,7 +273,9 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
     const unsigned parts = most < 1 ? 1u : most < gridDim.x ? static_cast<unsigned>(most) : gridDim.x;
     int64_t each;
     int rem;
-    if (base < (int64_t{1} << 32)) {   // 32-bit division takes a quarter of the time
+    if (most > 0 && most <= gridDim.x) {
+        each = odd ? 1 : kEvenTiles, rem = 0;
+    } else if (base < (int64_t{1} << 32)) {   // 32-bit division takes a quarter of the time
         const unsigned t = static_cast<unsigned>(base);
         each = t / parts, rem = static_cast<int>(t % parts);
     } else {
@@ -298,7 +301,7 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
         // the row tile of that sequence: 32 at a time
         int64_t off = sh.start_off;
         for (int r0 = 0; r0 < rts; r0 += 32) {
-            const int64_t u = r0 + lane < rts ? units_of(tile_keys(s, r0 + lane, a.H)) : 0;
+            const int64_t u = r0 + lane < rts ? units_of(tile_keys(a, s, r0 + lane)) : 0;
             const int64_t inc = warp_scan(u, lane);
             if (inc - u <= off && off < inc) {
                 sh.start_rt = r0 + lane;
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // rows past the sequence keep what the buffer held: their weights are zero
                     const int r0 = w.rt * kRows, rows = min(kRows, w.s.n * a.H - r0);
                     mbar_arrive_expect_tx(full, rows * kMlaWidth * 2);
-                    int t = r0 / a.H, h = r0 - t * a.H;
+                    int t = a.by_H.div(r0), h = r0 - t * a.H;
                     for (int r = 0; r < rows; r += a.q_box) {
                         if (a.q_box == kRows) {
                             tma_load_4d(sbase, &maps.q, full, 0, h, 0, w.s.row0 + t, pol);
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = min(kRows, w.s.n * a.H - r0);
             const bool whole = w.k0 == 0 && w.k1 == w.kt;
             auto visible = [&](int r) {
-                return r >= rows ? 0 : max(0, w.s.ctx - w.s.n + (r0 + r) / a.H + 1);
+                return r >= rows ? 0 : max(0, w.s.ctx - w.s.n + a.by_H.div(r0 + r) + 1);
             };
             const int vis_a = visible(ra), vis_b = visible(rb);
             float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
@@ -656,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the two warps of 16 rows take eight each
                 const int r = half ? rb : ra;
                 const float l = sh.half_of[0][r] + sh.half_of[1][r], m = half ? m_b : m_a;
-                const int t = (r0 + r) / a.H, h = r0 + r - t * a.H;
+                const int t = a.by_H.div(r0 + r), h = r0 + r - t * a.H;
                 if (whole) {
                     sh.factor[r] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
                     sh.row_off[r] = r < rows ? (w.s.row0 + t) * a.o_st + h * a.o_sh : -1;
@@ -855,7 +858,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
     };
     auto store = [&](const int4 &j, int r, int col, float4 acc, float M, float L) {
         const float inv = L > 0.f ? 1.0f / L : (L == 0.f ? 0.f : L);
-        const int t = (j.y + r) / a.H, h = j.y + r - t * a.H;
+        const int t = a.by_H.div(j.y + r), h = j.y + r - t * a.H;
         const int64_t q = j.x + t;
         T *dst = static_cast<T *>(a.out) + q * a.o_st + h * a.o_sh + col;
         *reinterpret_cast<uint2 *>(dst) = make_uint2(Elem<T>::pack(acc.x * inv, acc.y * inv), Elem<T>::pack(acc.z * inv, acc.w * inv));
@@ -952,6 +955,7 @@ cudaError_t launch_t(const PagedMaps &m, const PagedArgs &a, int grid, cudaStrea
 cudaError_t launch_paged(const PagedMaps &m, const PagedArgs &a, bool bf16, int grid, cudaStream_t stream) {
     if (grid > kMaxCtas) return cudaErrorInvalidValue;
     PagedArgs args = a;
+    args.by_H = Divisor(a.H), args.by_page = Divisor(a.page_size);
     const int64_t item_rows = std::min<int64_t>(kRows, (a.Tq * a.H + a.B - 1) / a.B);
     args.few_joins = static_cast<int>(kFewRows / std::max<int64_t>(item_rows, 1));
     return bf16 ? launch_t<__nv_bfloat16>(m, args, grid, stream) : launch_t<__half>(m, args, grid, stream);
