@@ -329,28 +329,6 @@ struct IssueWaiter {
 
 // ---------------------------------------------------------------- argument blocks
 
-struct RopeArgs {
-    const void *q;            // [T, H, dim], strides below (elements)
-    int64_t q_st, q_sh;
-    void *q_out;
-    int64_t qo_st, qo_sh;
-    const void *kv;           // [T, latent + dim]
-    int64_t kv_st;
-    const void *gamma;        // [latent] or NULL
-    void *kv_out;             // or NULL
-    int64_t kvo_st;
-    void *cache;              // or NULL
-    int64_t page_st, row_st;
-    int64_t num_pages;
-    int page_size;
-    const int32_t *slots;
-    const int32_t *positions;
-    const uint64_t *freq;
-    int T, H, dim, latent, layout;
-    float amplitude, eps;
-    unsigned int *err;
-};
-
 // Division of 0 <= x < 2^31 by a divisor known on the host, in three instructions instead of
 // twenty (Granlund and Montgomery, 1994): with 2^s >= d, m = floor(2^32 (2^s - d) / d) + 1,
 // x / d = (hi(x m) + x) >> s.
@@ -366,6 +344,29 @@ struct Divisor {
         return static_cast<int>((__umulhi(static_cast<uint32_t>(x), mul) + static_cast<uint32_t>(x)) >> shift);
     }
 #endif
+};
+
+struct RopeArgs {
+    const void *q;            // [T, H, dim], strides below (elements)
+    int64_t q_st, q_sh;
+    void *q_out;
+    int64_t qo_st, qo_sh;
+    const void *kv;           // [T, latent + dim]
+    int64_t kv_st;
+    const void *gamma;        // [latent] or NULL
+    void *kv_out;             // or NULL
+    int64_t kvo_st;
+    void *cache;              // or NULL
+    int64_t page_st, row_st;
+    int64_t num_pages;
+    int page_size;
+    Divisor by_page;          // (launch_t)
+    const int32_t *slots;
+    const int32_t *positions;
+    const uint64_t *freq;
+    int T, H, dim, latent, layout;
+    float amplitude, eps;
+    unsigned int *err;
 };
 
 struct PagedArgs {
@@ -405,6 +406,10 @@ struct ProjArgs {
     int T, H, K, N;
     int shared_x;             // x has one head that every output head reads
     int x_rows;               // rows of one load of x
+    // (launch_t) weight blocks of a head, token tiles, and a worker's tiles: each, one more
+    // for the first `longer`
+    int ntiles, ttiles, each, longer;
+    Divisor by_ntiles, by_ttiles;
     unsigned int *err;
 };
 

@@ -19,7 +19,7 @@ namespace {
 // memory, then TMA, which clips rows past T and columns past N) while the next one's
 // products run. W is read as it is stored, K or N contiguous: the descriptor, not a
 // copy, transposes it. Chunks past K, rows past T and columns past N arrive as zeros.
-// 256 tokens of 64 heads, 128 -> 512: 7.1 us, of which the first loads (2 us) and the last
+// 256 tokens of 64 heads, 128 -> 512: 6.8 us, of which the first loads (2 us) and the last
 // stores overlap nothing: 29 MB are 4.3 us of HBM.
 constexpr int kTile = 128;
 constexpr int kChunk = kTile * 128;      // 16 KB: 128 rows of 64 values
@@ -47,19 +47,16 @@ struct Line {
     bool keep;             // the blocks stay in shared memory over a run
     int blocks;
 
-    __device__ Line(const ProjArgs &a, int chunks, int worker, int workers, int rows, int blocks_) : blocks(blocks_) {
-        ttiles = (a.T + rows - 1) / rows;
-        const int64_t total = static_cast<int64_t>(ttiles) * (a.H * ntiles(a) / blocks);
-        at = static_cast<int>(total * worker / workers);
-        end = static_cast<int>(total * (worker + 1) / workers);
+    __device__ Line(const ProjArgs &a, int chunks, int worker, int blocks_) : ttiles(a.ttiles), blocks(blocks_) {
+        at = a.each * worker + min(worker, a.longer);
+        end = at + a.each + (worker < a.longer);
         keep = chunks <= kWSlots;
-        const int g = at / ttiles;
+        const int g = a.by_ttiles.div(at);
         tt = at - g * ttiles;
         block = g * blocks;
         first = true;
         last = !keep || at + 1 == end || tt + 1 == ttiles;
     }
-    static __host__ __device__ int ntiles(const ProjArgs &a) { return (a.N + kTile - 1) / kTile; }
     __device__ bool more() const { return at < end; }
     __device__ void next() {
         ++at;
@@ -80,7 +77,7 @@ template <typename T>
 __device__ __forceinline__ void store_tile(const ProjArgs &a, const CUtensorMap *map_out, uint32_t acc, uint32_t stage,
                                            int lane, int t, int block, bool ok) {
     using E = Elem<T>;
-    const int nt = Line::ntiles(a), h = block / nt, n0 = (block - h * nt) * kTile;
+    const int h = a.by_ntiles.div(block), n0 = (block - h * a.ntiles) * kTile;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t w[32];
@@ -143,8 +140,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t pol = policy_evict_normal();
             uint32_t xi = 0, wi = 0;   // chunks loaded
             bool ok = true;
-            for (Line l(a, chunks, blockIdx.x, gridDim.x, kTile, 1); l.more() && ok; l.next()) {
-                const int nt = Line::ntiles(a), h = l.block / nt, n0 = (l.block - h * nt) * kTile;
+            for (Line l(a, chunks, blockIdx.x, 1); l.more() && ok; l.next()) {
+                const int h = a.by_ntiles.div(l.block), n0 = (l.block - h * a.ntiles) * kTile;
                 for (int c = 0; c < chunks; ++c) {
                     if (l.first) {
                         const int st = wi % kWSlots;
@@ -186,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dw = KN ? sdesc_mn_sw128(sbase, kChunk / 2) : sdesc_sw128(sbase);
             uint32_t xi = 0, w0 = 0, n = 0;   // x chunks used; the block's first chunk; tiles
             bool ok = true;
-            for (Line l(a, chunks, blockIdx.x, gridDim.x, kTile, 1); l.more() && ok; l.next(), ++n) {
+            for (Line l(a, chunks, blockIdx.x, 1); l.more() && ok; l.next(), ++n) {
                 const uint32_t buf = n & 1;
                 if (!wait(smem_u32(&sh.acc_empty[buf]), ((n >> 1) & 1) ^ 1, ERR_WAIT_PART_EMPTY)) break;
 #pragma unroll 1
@@ -216,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16, stage = sbase + kOffOut + warp * (kChunk / 4);
         uint32_t n = 0;
         bool ok = true;
-        for (Line l(a, chunks, blockIdx.x, gridDim.x, kTile, 1); l.more(); l.next(), ++n) {
+        for (Line l(a, chunks, blockIdx.x, 1); l.more(); l.next(), ++n) {
             const uint32_t buf = n & 1;
             if (ok) ok = wait(smem_u32(&sh.acc_full[buf]), (n >> 1) & 1, ERR_WAIT_PART_FULL);
             __syncwarp();
@@ -274,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t tmem = 0;   // all 512 columns of both CTAs
     const Waiter wait{smem_u32(&sh.abort), a.err};
     const int chunks = (a.K + 63) / 64;
-    auto line = [&] { return Line(a, chunks, blockIdx.x / 2, gridDim.x / 2, 2 * kTile, 2); };
+    auto line = [&] { return Line(a, chunks, blockIdx.x / 2, 2); };
     pdl_wait();
 
     if (warp == 4) {
@@ -284,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t xi = 0, wi = 0;   // chunks loaded
             bool ok = true;
             for (Line l = line(); l.more() && ok; l.next()) {
-                const int nt = Line::ntiles(a), block = l.block + rank, h = block / nt, n0 = (block - h * nt) * kTile;
+                const int block = l.block + rank, h = a.by_ntiles.div(block), n0 = (block - h * a.ntiles) * kTile;
                 for (int c = 0; c < chunks; ++c) {
                     if (l.first) {
                         const int st = wi % kWSlots;
@@ -385,29 +382,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 // us. Where memory bounds it they lose to the 128-token tiles, which spread over twice as
 // many workers: 4096 tokens of 64 heads, 128 -> 512, 95 against 83 us.
 bool use_pairs(const ProjArgs &a) {
-    const int nt = Line::ntiles(a);
     const double T = a.T, H = a.H, K = a.K, N = a.N;
     const double bytes = 2.0 * (T * K * (a.shared_x ? 1.0 : H) + H * K * N + T * H * N);
-    return (a.shared_x ? a.H * nt : nt) % 2 == 0 && 2.0 * T * H * K * N > 350.0 * bytes;
+    return (a.shared_x ? a.H * a.ntiles : a.ntiles) % 2 == 0 && 2.0 * T * H * K * N > 350.0 * bytes;
 }
 
 template <typename T, bool KN>
-cudaError_t launch_t(const CUtensorMap &x, const CUtensorMap &w, const CUtensorMap &out, const ProjArgs &a, int num_sms,
+cudaError_t launch_t(const CUtensorMap &x, const CUtensorMap &w, const CUtensorMap &out, ProjArgs a, int num_sms,
                      cudaStream_t stream) {
+    a.ntiles = (a.N + kTile - 1) / kTile;
     const bool pairs = use_pairs(a);
     auto kernel = pairs ? head_proj_pair_kernel<T, KN> : head_proj_kernel<T, KN>;
     static std::atomic<uint64_t> done[2];
     cudaError_t e = allow_smem(kernel, kSmem, done[pairs]);
     if (e != cudaSuccess) return e;
     const int per = pairs ? 2 : 1, workers = num_sms / per;
-    const int64_t total = static_cast<int64_t>((a.T + per * kTile - 1) / (per * kTile)) * (a.H * Line::ntiles(a) / per);
+    a.ttiles = (a.T + per * kTile - 1) / (per * kTile);
+    const int64_t total = static_cast<int64_t>(a.ttiles) * (a.H * a.ntiles / per);
+    const int parts = total < workers ? static_cast<int>(total) : workers;
+    a.each = static_cast<int>(total / parts), a.longer = static_cast<int>(total % parts);
+    a.by_ntiles = Divisor(a.ntiles), a.by_ttiles = Divisor(a.ttiles);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(per * (total < workers ? static_cast<int>(total) : workers));
+    cfg.gridDim = dim3(per * parts);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;

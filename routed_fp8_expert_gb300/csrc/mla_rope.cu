@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) rope_append_kernel(co
         if (a.cache) {
             const int slot = a.slots[t];   // negative: this token is not cached
             if (slot >= 0) {
-                const unsigned page = static_cast<unsigned>(slot) / static_cast<unsigned>(a.page_size);
+                const unsigned page = a.by_page.div(slot);
                 if (page < a.num_pages)
                     row_cache = static_cast<T *>(a.cache) + page * a.page_st + (slot - page * a.page_size) * a.row_st;
                 else if (kvec == 0)
@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) rope_append_kernel(co
 }  // namespace
 
 template <typename T>
-static cudaError_t launch_t(const RopeArgs &a, cudaStream_t stream) {
+static cudaError_t launch_t(RopeArgs a, cudaStream_t stream) {
+    a.by_page = Divisor(a.cache ? a.page_size : 1);   // (without a cache it may be anything)
     if (a.dim == 64 && a.latent <= 8 * 128 && a.T > 8 * num_sms()) {
         auto kernel = a.layout ? rope_append_kernel<T, true, 64, 128> : rope_append_kernel<T, false, 64, 128>;
         return launch_pdl(kernel, dim3(a.T), dim3(128), 0, stream, a);
