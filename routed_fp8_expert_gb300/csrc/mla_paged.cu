@@ -28,7 +28,7 @@ namespace {
 // of two tiles covers that if a tile's way through it stays short: arrival (2,800 cycles
 // from HBM under load), scores, softmax, first products. For the same reason the two
 // products have their issuing warps, and eight warps share a tile's softmax. 256 sequences
-// of 4,246 keys on average: 220 us, 5.8 TB/s of what has to be read and written. Keys that
+// of 4,246 keys on average: 219 us, 5.9 TB/s of what has to be read and written. Keys that
 // many row tiles read come from L2, and shared memory is the bound: 240 KB that a tile's
 // MMAs read and 80 KB that are written for them take 2,560 cycles of the 2,760 per tile
 // (512 new tokens over 7,000 keys: 945 us, 0.97 PFLOP/s).
