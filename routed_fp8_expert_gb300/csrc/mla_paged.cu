@@ -50,7 +50,8 @@ constexpr int kOffP = kQBytes;
 constexpr int kOffPairs = kOffP + kRows * 128;
 constexpr int kOffRope = kOffPairs + kPairSlots * kPairBytes;
 constexpr int kOffMisc = kOffRope + kRopeSlots * kGroupBytes;
-constexpr int kSmem = kOffMisc + 2048;
+constexpr int kMisc = 2560;
+constexpr int kSmem = kOffMisc + kMisc;
 constexpr int kSoftWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kThreads = kSoftThreads + 128;     // + loads of keys and of queries, two MMA warps
@@ -83,7 +84,10 @@ struct Shared {
     uint64_t p_full, pv_done, q_full, q_empty, mma_done[2];
     uint32_t tmem;
     int abort;
-    float factor[kRows], half_of[2][kRows];
+    float factor[kRows];
+    // the two halves' maxima of a tile, and their sums of a segment: a segment of one tile has
+    // no barrier between a warp's read of its partner's maxima and the partner's sums
+    float half_of[2][kRows], sum_of[2][kRows];
     int64_t row_off[kRows];
     int64_t warp_sum[kThreads / 32];
     // the line of key tiles: CTA c's part starts at each * c + min(c, rem)
@@ -91,7 +95,7 @@ struct Shared {
     int rem, start_b, start_rt;
     Seq start;
 };
-static_assert(sizeof(Shared) <= 2048, "");
+static_assert(sizeof(Shared) <= kMisc, "");
 
 // Queries and visible keys of sequence b. A length or offset outside its buffer is
 // recorded once and leaves the sequence without rows.
@@ -653,12 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l_b += __shfl_xor_sync(0xffffffffu, l_b, o);
             }
             const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
-            if ((lane & 3) == 0) sh.half_of[half][ra] = l_a, sh.half_of[half][rb] = l_b;
+            if ((lane & 3) == 0) sh.sum_of[half][ra] = l_a, sh.sum_of[half][rb] = l_b;
             named_bar_sync(1, kSoftThreads);   // factor and row_off are free again, too
             if ((lane & 3) == 0) {
                 // the two warps of 16 rows take eight each
                 const int r = half ? rb : ra;
-                const float l = sh.half_of[0][r] + sh.half_of[1][r], m = half ? m_b : m_a;
+                const float l = sh.sum_of[0][r] + sh.sum_of[1][r], m = half ? m_b : m_a;
                 const int t = a.by_H.div(r0 + r), h = r0 + r - t * a.H;
                 if (whole) {
                     sh.factor[r] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);

@@ -310,6 +310,22 @@ def test_paged_short_batches(ctx, H):
     check(lse, rl, lb, "lse")
 
 
+@pytest.mark.parametrize("ctx,H", [([64] * 150, 64), ([9 + i % 50 for i in range(151)], 33), ([64 * 151], 64), ([64 * 37 - 5] * 4, 64)])
+def test_paged_single_tile_segments_repeat(ctx, H):
+    # every CTA has one key tile: the exchange of the two halves' maxima, then at once of their sums
+    n = [1] * len(ctx)
+    q, cache, table, ctx_t = paged_inputs(ctx, n, H, 64, seed=len(ctx) + H, junk=math.nan)
+    args = [x.to(DEV) for x in (q, cache, table, ctx_t)]
+    ws = moe.mla_paged_workspace(DEV)
+    o, lse = moe.mla_attn_paged(*args, SCALE, want_lse=True, ws=ws)
+    ro, rl, ob, lb = paged_ref(q, cache, table, ctx_t, n, BF16)
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
+    again = [moe.mla_attn_paged(*args, SCALE, want_lse=True, ws=ws) for _ in range(200)]
+    assert all(torch.equal(o, x) and torch.equal(lse, y) for x, y in again)
+    assert error_word() == (_lib.MOE_OK, 0)
+
+
 def test_paged_views_and_strides():
     ctx, n, H = [150, 90], [1, 1], 8
     q, cache, table, ctx_t = paged_inputs(ctx, n, H, 32, seed=11)

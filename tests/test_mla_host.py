@@ -2,6 +2,8 @@
 No GPU: bad arguments are turned away before anything is enqueued."""
 import ctypes
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -119,3 +121,29 @@ def test_binding_wants_cuda_tensors():
     x = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         moe.mla_head_proj(x, torch.zeros(4, 8, 128, dtype=torch.bfloat16))
+
+
+def test_paged_exchanges_of_a_single_tile_are_separated_by_barriers():
+    # Two warps of a tile exchange values through shared arrays: each writes its [half] and
+    # reads the other's. In a segment of one key tile (nothing behind `if (j > 0)` runs) the
+    # next write of an array has to stand behind a barrier that follows its last read.
+    with open(os.path.join(build.CSRC, "mla_paged.cu")) as f:
+        src = f.read()
+    body = src[src.index("softmax and results"):src.index("the segment's result")]
+    out = src[src.index("the segment's result"):src.index("Joins the partial results")]
+    first = re.search(r"if \(j > 0\) \{", body)
+    depth, end = 1, first.end()
+    while depth:
+        depth += {"{": 1, "}": -1}.get(body[end], 0)
+        end += 1
+    text = body[:first.start()] + body[end:] + out
+    pending, writes = set(), 0                               # arrays read since the last barrier
+    for m in re.finditer(r"(named_bar_(?:sync|or)\()|sh\.(\w+)\[half\]\[\w+\] = |sh\.(\w+)\[(?:half \^ 1|0|1)\]\[", text):
+        if m[1]:
+            pending.clear()
+        elif m[2]:
+            writes += 1
+            assert m[2] not in pending, f"{m[2]} is written before its last values are read everywhere"
+        else:
+            pending.add(m[3])
+    assert writes == 4                                       # both rows' maxima, both rows' sums
