@@ -373,6 +373,11 @@ int mla_head_proj(const void *x, int64_t x_st, int64_t x_sh, int x_shared, const
                   int64_t w_sr, int w_kn, int T, int H, int K, int N, int dtype, void *out, int64_t o_st,
                   int64_t o_sh, void *stream);
 
+/* The form mla_head_proj takes for these sizes: 1 pairs of CTAs with 256 x 256 output
+ * tiles (long inputs, where the tensor rate bounds the call), 0 single CTAs with 128 x 128;
+ * a negative MOE_ERR_* for sizes that it refuses. Touches no device. */
+int mla_head_proj_form(int T, int H, int K, int N, int x_shared);
+
 /* Reads and clears the device error word of the current device after
  * synchronising `stream`. MOE_ERR_TIMEOUT if a kernel's bounded wait on an
  * mbarrier gave up since the last check (bits 0x01..0x10, 0x40; its outputs are

@@ -68,6 +68,7 @@ _SIGS = {
                                  _c_i64, _c_i64, _vp, _vp]),
     "mla_head_proj": (_c_int, [_vp, _c_i64, _c_i64, _c_int, _vp, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int,
                                _c_int, _c_int, _vp, _c_i64, _c_i64, _vp]),
+    "mla_head_proj_form": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int]),
     "moe_check_device_error": (_c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "moe_test_wait_timeout": (_c_int, [ctypes.c_uint64, _vp]),
     "moe_last_error_string": (ctypes.c_char_p, []),

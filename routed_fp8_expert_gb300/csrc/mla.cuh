@@ -423,6 +423,7 @@ struct PagedMaps {
 cudaError_t launch_paged(const PagedMaps &m, const PagedArgs &a, bool bf16, int grid, cudaStream_t stream);
 cudaError_t launch_ragged(const CUtensorMap &q, const CUtensorMap &k_nope, const CUtensorMap &k_pe,
                           const CUtensorMap &v, const RaggedArgs &a, bool bf16, cudaStream_t stream);
+bool proj_uses_pairs(int T, int H, int K, int N, bool shared_x);
 cudaError_t launch_proj(const CUtensorMap &x, const CUtensorMap &w, const CUtensorMap &out, const ProjArgs &a, bool bf16,
                         bool w_kn, int num_sms, cudaStream_t stream);
 

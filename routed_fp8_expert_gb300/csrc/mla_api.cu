@@ -88,6 +88,15 @@ int tensor_map(CUtensorMap *m, const void *p, int dtype, int rank, const int64_t
     return MOE_OK;
 }
 
+int proj_sizes(int T, int H, int K, int N) {
+    MLA_CHECK(range(H, 1, 1024, "H"));
+    if (K < 8 || K > 8192 || K % 8) return fail(MOE_ERR_UNSUPPORTED, "K=%d must be a multiple of 8 in [8, 8192]", K);
+    if (N < 8 || N > 8192 || N % 8) return fail(MOE_ERR_UNSUPPORTED, "N=%d must be a multiple of 8 in [8, 8192]", N);
+    MLA_CHECK(count(T, "T"));
+    MLA_CHECK(range(T, 0, 1 << 20, "T"));
+    return MOE_OK;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 int scale_ok(float scale) {
@@ -349,11 +358,7 @@ int mla_head_proj(const void *x, int64_t x_st, int64_t x_sh, int x_shared, const
     MLA_CHECK(dtype_ok(dtype));
     if (x_shared != 0 && x_shared != 1) return fail(MOE_ERR_ARG, "x_shared=%d must be 0 or 1", x_shared);
     if (w_kn != 0 && w_kn != 1) return fail(MOE_ERR_ARG, "w_kn=%d must be 0 or 1", w_kn);
-    MLA_CHECK(range(H, 1, 1024, "H"));
-    if (K < 8 || K > 8192 || K % 8) return fail(MOE_ERR_UNSUPPORTED, "K=%d must be a multiple of 8 in [8, 8192]", K);
-    if (N < 8 || N > 8192 || N % 8) return fail(MOE_ERR_UNSUPPORTED, "N=%d must be a multiple of 8 in [8, 8192]", N);
-    MLA_CHECK(count(T, "T"));
-    MLA_CHECK(range(T, 0, 1 << 20, "T"));
+    MLA_CHECK(proj_sizes(T, H, K, N));
     if (T == 0) return MOE_OK;
     MLA_CHECK(ptr(x, "x"));
     MLA_CHECK(stride(x_st, 8, "x_st"));
@@ -391,6 +396,13 @@ int mla_head_proj(const void *x, int64_t x_st, int64_t x_sh, int x_shared, const
              "head projection launch");
     report_launches(1);
     return MOE_OK;
+}
+
+int mla_head_proj_form(int T, int H, int K, int N, int x_shared) {
+    report_launches(0);
+    if (x_shared != 0 && x_shared != 1) return fail(MOE_ERR_ARG, "x_shared=%d must be 0 or 1", x_shared);
+    MLA_CHECK(proj_sizes(T, H, K, N));
+    return T > 0 && proj_uses_pairs(T, H, K, N, x_shared != 0) ? 1 : 0;
 }
 
 }  // extern "C"

@@ -376,22 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 5) pair_tmem_dealloc<512>(sh.tmem);
 }
 
-// Pairs take two weight blocks that read the same x: an even number of a head's, or of all
-// when the heads share x. They win where the tensor rate bounds the call (from 350 flops
-// per byte; the GPU's own ratio is 270): 4096 tokens of 512 -> 64 x 256, shared, 66 -> 51
-// us. Where memory bounds it they lose to the 128-token tiles, which spread over twice as
-// many workers: 4096 tokens of 64 heads, 128 -> 512, 95 against 83 us.
-bool use_pairs(const ProjArgs &a) {
-    const double T = a.T, H = a.H, K = a.K, N = a.N;
-    const double bytes = 2.0 * (T * K * (a.shared_x ? 1.0 : H) + H * K * N + T * H * N);
-    return (a.shared_x ? a.H * a.ntiles : a.ntiles) % 2 == 0 && 2.0 * T * H * K * N > 350.0 * bytes;
-}
-
 template <typename T, bool KN>
 cudaError_t launch_t(const CUtensorMap &x, const CUtensorMap &w, const CUtensorMap &out, ProjArgs a, int num_sms,
                      cudaStream_t stream) {
     a.ntiles = (a.N + kTile - 1) / kTile;
-    const bool pairs = use_pairs(a);
+    const bool pairs = proj_uses_pairs(a.T, a.H, a.K, a.N, a.shared_x);
     auto kernel = pairs ? head_proj_pair_kernel<T, KN> : head_proj_kernel<T, KN>;
     static std::atomic<uint64_t> done[2];
     cudaError_t e = allow_smem(kernel, kSmem, done[pairs]);
@@ -418,6 +407,18 @@ cudaError_t launch_t(const CUtensorMap &x, const CUtensorMap &w, const CUtensorM
 }
 
 }  // namespace
+
+// Pairs take two weight blocks that read the same x: an even number of a head's, or of all
+// when the heads share x. They win where the tensor rate bounds the call (from 350 flops
+// per byte; the GPU's own ratio is 270): 4096 tokens of 512 -> 64 x 256, shared, 66 -> 51
+// us. Where memory bounds it they lose to the 128-token tiles, which spread over twice as
+// many workers: 4096 tokens of 64 heads, 128 -> 512, 95 against 83 us.
+bool proj_uses_pairs(int T, int H, int K, int N, bool shared_x) {
+    const double t = T, h = H, k = K, n = N;
+    const double bytes = 2.0 * (t * k * (shared_x ? 1.0 : h) + h * k * n + t * h * n);
+    const int ntiles = (N + kTile - 1) / kTile;
+    return (shared_x ? H * ntiles : ntiles) % 2 == 0 && 2.0 * t * h * k * n > 350.0 * bytes;
+}
 
 cudaError_t launch_proj(const CUtensorMap &x, const CUtensorMap &w, const CUtensorMap &out, const ProjArgs &a, bool bf16,
                         bool w_kn, int num_sms, cudaStream_t stream) {

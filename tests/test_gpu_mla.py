@@ -67,6 +67,29 @@ def test_head_proj_of_long_inputs(T, H, K, N, shared, w_kn, dtype):
     assert (buf[T] == 3.0).all() and (buf[:, :, N:] == 3.0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("w_kn", [False, True])
+@pytest.mark.parametrize("T,H,K,N,shared", [
+    (1281, 2, 1024, 1024, False),                            # weights through the ring; one row in the last tile
+    (3001, 2, 776, 1000, False),                             # partial chunks, token tiles and weight blocks
+    (2049, 10, 512, 264, True),                              # three weight blocks a head: pairs span two heads
+    (1500, 24, 512, 256, True), (1100, 24, 640, 136, True),
+])
+def test_head_proj_of_cta_pairs(T, H, K, N, shared, w_kn, dtype):
+    assert moe.load().mla_head_proj_form(T, H, K, N, int(shared)) == 1
+    x = randn(T, 1 if shared else H, K + 8, seed=T, dtype=dtype)[..., :K]
+    w = randn(*((H, K, N) if w_kn else (H, N, K)), seed=K, dtype=dtype, std=K ** -0.5)
+    buf = torch.full((T + 1, H, N + 8), 3.0, dtype=dtype, device=DEV)
+    y = moe.mla_head_proj(x.to(DEV), w.to(DEV), w_kn=w_kn, out=buf[:T, :, :N])
+    assert error_word() == (_lib.MOE_OK, 0)
+    xd, wd = x.double().expand(T, H, K).transpose(0, 1), w.double() if w_kn else w.double().transpose(1, 2)
+    ref = torch.bmm(xd, wd).transpose(0, 1)
+    mag = torch.bmm(xd.abs(), wd.abs()).transpose(0, 1)
+    check(y, ref, rounding(dtype, ref) + (K / 16 + 8) * 2.0 ** -23 * mag, "out")
+    assert (buf[T] == 3.0).all() and (buf[:, :, N:] == 3.0).all()
+    assert torch.equal(y, moe.mla_head_proj(x.to(DEV), w.to(DEV), w_kn=w_kn))
+
+
 def test_head_proj_reads_views_in_place():
     # one up-projection weight [H, 256, 512] holds the key and the value halves of each
     # head; the absorb product reads the key half with K contiguous rows swapped

@@ -108,6 +108,16 @@ def test_refusals(lib, call, base, change, code):
     assert lib.moe_last_error_string() and lib.moe_last_launch_count() == 0
 
 
+@pytest.mark.parametrize("T,H,K,N,shared,form", [
+    (4096, 64, 512, 256, 1, 1), (1500, 64, 512, 256, 1, 1), (2049, 10, 512, 264, 1, 1), (1281, 2, 1024, 1024, 0, 1),
+    (4096, 64, 128, 512, 0, 0), (1, 64, 512, 256, 1, 0), (0, 64, 512, 256, 1, 0),
+    (2000, 4, 1024, 1152, 0, 0), (3001, 9, 1024, 264, 1, 0),   # an odd number of weight blocks
+    (-1, 4, 128, 128, 0, ARG), (4, 4, 128, 128, 2, ARG), (4, 0, 128, 128, 0, UNS), (4, 4, 12, 128, 0, UNS), (4, 4, 128, 8200, 1, UNS),
+])
+def test_head_proj_form(lib, T, H, K, N, shared, form):
+    assert lib.mla_head_proj_form(T, H, K, N, shared) == form
+
+
 def test_nothing_to_do(lib):
     assert lib.mla_rope_append(*dict(ROPE, T=0, q=None, positions=None).values()) == _lib.MOE_OK
     assert lib.mla_attn_paged(*dict(PAGED, B=0, Tq=0, q=None, ctx=None).values()) == _lib.MOE_OK
