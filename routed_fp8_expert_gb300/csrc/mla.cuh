@@ -240,6 +240,15 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// sum += x with what rounding loses kept in `lost` and added to the next x (Kahan, 1965). A
+// softmax's sum takes a tile's weights at a time: beside one weight of 1, 131,072 keys of 2^-24
+// each would otherwise be rounded at half their size (lse off by 3e-4).
+__device__ __forceinline__ void add_compensated(float &sum, float &lost, float x) {
+    const float y = x + lost, t = sum + y;
+    lost = y - (t - sum);
+    sum = t;
+}
+
 // Move registers between the launch's warpgroups (all 128 threads of one execute it).
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }

@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return r >= rows ? 0 : max(0, w.s.ctx - w.s.n + a.by_H.div(r0 + r) + 1);
             };
             const int vis_a = visible(ra), vis_b = visible(rb);
-            float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
+            float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f, lost_a = 0.f, lost_b = 0.f;
             for (int j = 0; j < n; ++j, ++tile) {
                 const uint32_t buf = tile & 1, ph = (tile >> 1) & 1;
                 hold(&sh.s_full[buf], ph, ERR_WAIT_PART_FULL);
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float na = fmaxf(m_a, fmaxf(mx_a, sh.half_of[half ^ 1][ra]));
                     const float nb = fmaxf(m_b, fmaxf(mx_b, sh.half_of[half ^ 1][rb]));
                     const float fa = m_a == -INFINITY ? 0.f : ex2(m_a - na), fb = m_b == -INFINITY ? 0.f : ex2(m_b - nb);
-                    l_a *= fa, l_b *= fb;
+                    l_a *= fa, l_b *= fb, lost_a *= fa, lost_b *= fb;
                     m_a = na, m_b = nb;
                     if (j > 0) {
                         if (half == 0 && (lane & 3) == 0) sh.factor[ra] = fa, sh.factor[rb] = fb;
@@ -618,19 +618,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float ea = m_a == -INFINITY ? 0.f : m_a, eb = m_b == -INFINITY ? 0.f : m_b;
                 uint32_t pa[4], pb[4];
+                float s_a = 0.f, s_b = 0.f;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const float a0 = ex2(fmaf(__uint_as_float(r[4 * g]), a.scale_log2, -ea));
                     const float a1 = ex2(fmaf(__uint_as_float(r[4 * g + 1]), a.scale_log2, -ea));
                     const float b0 = ex2(fmaf(__uint_as_float(r[4 * g + 2]), a.scale_log2, -eb));
                     const float b1 = ex2(fmaf(__uint_as_float(r[4 * g + 3]), a.scale_log2, -eb));
-                    l_a += a0 + a1;
-                    l_b += b0 + b1;
+                    s_a += a0 + a1;
+                    s_b += b0 + b1;
                     // the weights enter the second product in the tensors' 16-bit type:
                     // half an ulp each, averaged over the keys
                     pa[g] = E::pack(a0, a1);
                     pb[g] = E::pack(b0, b1);
                 }
+                add_compensated(l_a, lost_a, s_a);
+                add_compensated(l_b, lost_b, s_b);
                 if (tile > 0) hold(&sh.pv_done, (tile - 1) & 1, ERR_WAIT_PART_FULL);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -651,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_u32(&sh.p_full));
             }
             // -------------------------------------------------- the segment's result
+            l_a += lost_a, l_b += lost_b;
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
                 l_a += __shfl_xor_sync(0xffffffffu, l_a, o);

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int vis = valid ? visible(row) : 0;
         // tiles that every row of the warp sees whole need no mask
         const int vis_min = __reduce_min_sync(0xffffffffu, vis);
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, lost = 0.f;
         bool ok = true;
         auto hold = [&](uint64_t *bar, uint32_t parity, uint32_t bit) {
             if (ok) ok = wait(smem_u32(bar), parity, bit);
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, behind)) {
                     const float mn = fmaxf(m, mx);
                     const float f = m == -INFINITY ? 0.f : ex2(m - mn);
-                    l *= f;
+                    l *= f, lost *= f;
                     m = mn;
                     if (j > 0) {
                         // S_t of this tile was issued after P_t V of the one before, and
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float2 both = unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])));
-                l += both.x + both.y;
+                add_compensated(l, lost, both.x + both.y);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sh.p_full[t][1]));
@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 tc_fence_after();
             }
+            l += lost;
             const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
             // Results leave through the row tile's query buffer (its scores are done): a
             // thread holds a row, and rows are far apart in memory, so that 16-byte stores

@@ -306,6 +306,24 @@ def test_paged_rising_scores_move_the_reference_maximum():
     check(lse, rl, lb, "falling lse")
 
 
+@pytest.mark.parametrize("gap", [1.2, 16.0, 17.0, 17.5])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_paged_lse_of_many_small_weights(dtype, gap):
+    # 131,072 keys at weights near e^-gap of the first one's, in one running sum: as many
+    # sequences as processors, so that no item is split
+    n, page, B = 131072, 64, torch.cuda.get_device_properties(0).multi_processor_count
+    cache = randn(n // page, page, 576, seed=1, dtype=dtype, std=0.1)
+    q = torch.zeros(1, 2, 576, dtype=dtype)
+    q[..., 513:] = randn(1, 2, 63, seed=2, dtype=dtype, std=0.1)
+    q[..., 512], cache[..., 512] = 16.0, 0.0
+    cache[0, 0, 512] = gap / (16 * SCALE)
+    table, ctx = torch.arange(n // page, dtype=torch.int32), torch.full((B,), n, dtype=torch.int32)
+    _, lse = run_paged(q.expand(B, 2, 576).contiguous(), cache, table.expand(B, n // page).contiguous(), ctx, [1] * B)
+    assert error_word() == (_lib.MOE_OK, 0)
+    _, rl, _, lb = paged_ref(q, cache, table[None], ctx[:1], [1], dtype)
+    check(lse, rl.expand(B, 2), lb.expand(B, 2), "lse")
+
+
 def test_paged_long_context_is_split_and_joined():
     ctx, n = [20000, 3, 9000], [1, 1, 2]
     q, cache, table, ctx_t = paged_inputs(ctx, n, 16, 64, seed=9)
@@ -506,6 +524,21 @@ def test_ragged_rising_scores_move_the_reference_maximum():
         ro, rl, ob, lb = ragged_ref(q * sign, kv[..., :128], kp, kv[..., 128:], [n], [n], True, BF16)
         check(o, ro, ob, "out")
         check(lse, rl, lb, "lse")
+
+
+@pytest.mark.parametrize("gap", [1.2, 16.0, 17.0, 17.5])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_ragged_lse_of_many_small_weights(dtype, gap):
+    n, nq = 131072, 3
+    q, kv, kp = torch.zeros(nq, 1, 192, dtype=dtype), randn(n, 1, 256, seed=1, dtype=dtype, std=0.1), randn(n, 64, seed=2, dtype=dtype, std=0.1)
+    q[..., 128:] = randn(nq, 1, 64, seed=3, dtype=dtype, std=0.1)
+    q[..., 0], kv[..., 0], kv[0, :, 0] = 16.0, 0.0, gap / (16 * SCALE)
+    kvd = kv.to(DEV)
+    _, lse = moe.mla_attn_ragged(q.to(DEV), kvd[..., :128], kp.to(DEV), kvd[..., 128:], offsets([nq]), offsets([n]), nq,
+                                 SCALE, causal=False, want_lse=True)
+    assert error_word() == (_lib.MOE_OK, 0)
+    _, rl, _, lb = ragged_ref(q, kv[..., :128], kp, kv[..., 128:], [nq], [n], False, dtype)
+    check(lse, rl, lb, "lse")
 
 
 def test_ragged_strides_and_output_view():
