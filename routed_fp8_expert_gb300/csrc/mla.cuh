@@ -17,9 +17,15 @@ constexpr int kMlaWidth = kMlaLatent + kMlaRope;
 constexpr int kMlaNope = 128;
 constexpr int kMlaV = 128;
 
+// kLift: the softmax weights are 2^(score - reference), the reference kLift below the running
+// maximum. fp16 weights start at 2^7: below 2^-14 their rounding is absolute and below 2^-25
+// nothing is left, which many far keys beside one that dominates would notice (131,072 keys
+// of 2^-25 of the largest weight are 0.4% of the sum; 2^-7 of that step is below the rounding
+// of the result). With the lag of 2^8 a weight reaches 2^15 of the 65,504 that fit.
 template <typename T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
     static constexpr uint32_t kFmt = 1;   // kind::f16 operand format
+    static constexpr float kLift = 0.f;
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&v);
@@ -31,6 +37,7 @@ template <> struct Elem<__nv_bfloat16> {
 };
 template <> struct Elem<__half> {
     static constexpr uint32_t kFmt = 0;
+    static constexpr float kLift = 7.f;
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         const __half2 v = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&v);

@@ -13,7 +13,7 @@ namespace {
 // The (token, head) rows of a sequence are flattened (row = token * H + head) and cut
 // into tiles of 64; keys come in tiles of 64. For one pair of tiles
 //   S [64 rows, 64 keys]  = Q K^T          9 column groups of 64, M = 64, N = 64
-//   P = 2^(S scale - m)                     m: the row's reference maximum
+//   P = 2^(S scale - m)                     m: the row's reference (its maximum, less Elem::kLift)
 //   O^T [512, 64 rows]   += C^T P^T        4 blocks of 128 latent columns, M = 128, N = 64
 // The latent columns of the key tile serve both products from one copy in shared
 // memory: as B of the first (keys x columns, columns contiguous) and, transposed, as A
@@ -57,9 +57,10 @@ constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kThreads = kSoftThreads + 128;     // + loads of keys and of queries, two MMA warps
 constexpr int kTmemO = 0;                        // 4 x 64 columns
 constexpr int kTmemS = 256;                      // 2 x 64 columns
-// A row's reference maximum follows its running maximum only when it falls behind by
-// more than 2^8: the sums then stay below 2^8 times their true scale, far from
-// overflow, and O is rescaled a few times per item instead of once per tile.
+// A row's reference follows its running maximum only when that has risen by more than
+// 2^8: the sums then stay below 2^8 times their true scale, far from overflow, and O is
+// rescaled a few times per item instead of once per tile. (Differences are compared: at
+// references where 8 is less than the spacing of fp32 a sum would round past it.)
 constexpr float kLag = 8.0f;
 constexpr int kNoPage = -0x7fffffff - 1;
 // Fewest key tiles a CTA is given: one, unless every item has an even number of them. Then
@@ -589,12 +590,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, o));
                 }
                 mx_a *= a.scale_log2, mx_b *= a.scale_log2;
-                const bool behind = mx_a > m_a + kLag || mx_b > m_b + kLag;
+                const bool behind = mx_a - m_a > E::kLift + kLag || mx_b - m_b > E::kLift + kLag;
                 if (named_bar_or(1, kSoftThreads, behind)) {
                     if ((lane & 3) == 0) sh.half_of[half][ra] = mx_a, sh.half_of[half][rb] = mx_b;
                     named_bar_sync(1, kSoftThreads);
-                    const float na = fmaxf(m_a, fmaxf(mx_a, sh.half_of[half ^ 1][ra]));
-                    const float nb = fmaxf(m_b, fmaxf(mx_b, sh.half_of[half ^ 1][rb]));
+                    const float na = fmaxf(m_a, fmaxf(mx_a, sh.half_of[half ^ 1][ra]) - E::kLift);
+                    const float nb = fmaxf(m_b, fmaxf(mx_b, sh.half_of[half ^ 1][rb]) - E::kLift);
                     const float fa = m_a == -INFINITY ? 0.f : ex2(m_a - na), fb = m_b == -INFINITY ? 0.f : ex2(m_b - nb);
                     l_a *= fa, l_b *= fb, lost_a *= fa, lost_b *= fb;
                     m_a = na, m_b = nb;
@@ -628,7 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     s_a += a0 + a1;
                     s_b += b0 + b1;
                     // the weights enter the second product in the tensors' 16-bit type:
-                    // half an ulp each, averaged over the keys
+                    // half an ulp each, averaged over the keys (fp16: down to 2^-21 of
+                    // the largest, from there an absolute 2^-32 of it)
                     pa[g] = E::pack(a0, a1);
                     pb[g] = E::pack(b0, b1);
                 }

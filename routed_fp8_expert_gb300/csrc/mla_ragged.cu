@@ -11,7 +11,7 @@ namespace {
 // One CTA takes 256 query rows of one head as two tiles of 128 and walks the sequence's
 // keys in tiles of 128 with the running maximum and sum of a softmax:
 //   S_t [128, 128]  = Q_t K^T      M = 128, N = 128, 192 columns (128 + the shared 64)
-//   P_t = 2^(S_t scale - m)
+//   P_t = 2^(S_t scale - m)         m: the row's reference (its maximum, less Elem::kLift)
 //   O_t [128, 128] += P_t V        P_t in tensor memory, V with its columns contiguous
 // The two tiles alternate: while one's scores pass through the exponentials, the other's
 // products run. Both read one copy of the keys and values. K and V arrive in 16 KB
@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     top[c] = fmaxf(top[c], __uint_as_float(r[c][31]));
                 }
                 const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-                const bool behind = mx > m + kLag;
+                const bool behind = mx - m > E::kLift + kLag;
                 if (__any_sync(0xffffffffu, behind)) {
-                    const float mn = fmaxf(m, mx);
+                    const float mn = fmaxf(m, mx - E::kLift);
                     const float f = m == -INFINITY ? 0.f : ex2(m - mn);
                     l *= f, lost *= f;
                     m = mn;
@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float p0 = ex2(x.x), p1 = ex2(x.y);
                             sum[(i / 2) & 3] = add_f32x2(sum[(i / 2) & 3], pack_f32x2(p0, p1));
                             // the weights enter the second product in the tensors' 16-bit
-                            // type: half an ulp each, averaged over the keys
+                            // type: half an ulp each, averaged over the keys (fp16: down to
+                            // 2^-21 of the largest, from there an absolute 2^-32 of it)
                             p[c * 16 + i / 2] = E::pack(p0, p1);
                         }
                     tmem_st32(ts + hh * 32, p);

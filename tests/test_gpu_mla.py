@@ -27,6 +27,12 @@ def error_word():
     return st, detail.value
 
 
+def added_up(n, mag):
+    """What n products added in tensor memory may lose, by _mla_ref's model: 16 at a time, truncating
+    fp32 adds. mag: the sum of their magnitudes. (_mla_ref.attention's 2^-18 holds it up to 384 keys.)"""
+    return (n / 16 + 8) * 2.0 ** -23 * mag
+
+
 # ------------------------------------------------------------------ projections
 
 @pytest.mark.parametrize("dtype", [BF16, FP16])
@@ -324,6 +330,47 @@ def test_paged_lse_of_many_small_weights(dtype, gap):
     check(lse, rl.expand(B, 2), lb.expand(B, 2), "lse")
 
 
+@pytest.mark.parametrize("gap", [17.0, 17.5, 20.0])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_paged_one_key_far_above_many(dtype, gap):
+    # 131,072 keys of weights near e^-gap of the first one's: each is next to nothing, together
+    # they are not (e^-17.33 is 2^-25, where a weight below one vanishes in fp16). As many
+    # sequences as processors, so that no item is split.
+    n, page, B = 131072, 64, torch.cuda.get_device_properties(0).multi_processor_count
+    cache = randn(n // page, page, 576, seed=1, dtype=dtype, std=0.1)
+    cache[..., :512] += 1.0
+    cache[0, 0, :512] = -0.05
+    q = torch.zeros(1, 2, 576, dtype=dtype)
+    q[..., 513:] = randn(1, 2, 63, seed=2, dtype=dtype)
+    q[..., 512], cache[..., 512] = 16.0, 0.0
+    cache[0, 0, 512] = gap / (16 * SCALE)
+    table, ctx = torch.arange(n // page, dtype=torch.int32), torch.full((B,), n, dtype=torch.int32)
+    o, lse = run_paged(q.expand(B, 2, 576).contiguous(), cache, table.expand(B, n // page).contiguous(), ctx, [1] * B)
+    assert error_word() == (_lib.MOE_OK, 0)
+    ro, rl, ob, lb = paged_ref(q, cache, table[None], ctx[:1], [1], dtype)
+    keys = cache.view(n, 576)
+    ob = ob + added_up(n, attention(q[0], keys, keys[:, :512].abs(), [n, n], SCALE, dtype)[0])
+    check(o, ro.expand(B, 2, 512), ob.expand(B, 2, 512), "out")
+    check(lse, rl.expand(B, 2), lb.expand(B, 2), "lse")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("L", [900, 30000])
+def test_paged_rising_scores_in_both_types(L, dtype):
+    # the reference maximum moves in every tile, up to weights near the largest that fit the
+    # type; the long one is split and joined
+    q, cache, table, ctx_t = paged_inputs([L], [1], 64, 64, seed=8, dtype=dtype)
+    for step in (0.02, 0.6, 4.0):
+        for i, p in enumerate(table[0, :(L + 63) // 64].tolist()):
+            cache[p] = cache[p].clamp(-1, 1)
+            cache[p, :, 0] = ((torch.arange(64) + i * 64) * (900 / L)).to(dtype)
+        q[..., 0] = step
+        o, lse = run_paged(q, cache, table, ctx_t, [1])
+        ro, rl, ob, lb = paged_ref(q, cache, table, ctx_t, [1], dtype)
+        check(o, ro, ob, "out")
+        check(lse, rl, lb, "lse")
+
+
 def test_paged_long_context_is_split_and_joined():
     ctx, n = [20000, 3, 9000], [1, 1, 2]
     q, cache, table, ctx_t = paged_inputs(ctx, n, 16, 64, seed=9)
@@ -539,6 +586,42 @@ def test_ragged_lse_of_many_small_weights(dtype, gap):
     assert error_word() == (_lib.MOE_OK, 0)
     _, rl, _, lb = ragged_ref(q, kv[..., :128], kp, kv[..., 128:], [nq], [n], False, dtype)
     check(lse, rl, lb, "lse")
+
+
+@pytest.mark.parametrize("gap", [17.0, 17.5, 20.0])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_ragged_one_key_far_above_many(dtype, gap):
+    # 131,072 keys of weights near e^-gap of the first one's: each is next to nothing, together
+    # they are not (e^-17.33 is 2^-25, where a weight below one vanishes in fp16)
+    n, nq = 131072, 3
+    q, kv, kp = torch.zeros(nq, 1, 192, dtype=dtype), randn(n, 1, 256, seed=1, dtype=dtype, std=0.1), randn(n, 64, seed=2, dtype=dtype, std=0.1)
+    kv[..., 128:] += 1.0
+    kv[0, :, 128:] = -0.05
+    q[..., 128:] = randn(nq, 1, 64, seed=3, dtype=dtype)
+    q[..., 0], kv[..., 0], kv[0, :, 0] = 16.0, 0.0, gap / (16 * SCALE)
+    kvd = kv.to(DEV)
+    o, lse = moe.mla_attn_ragged(q.to(DEV), kvd[..., :128], kp.to(DEV), kvd[..., 128:], offsets([nq]), offsets([n]), nq,
+                                 SCALE, causal=False, want_lse=True)
+    assert error_word() == (_lib.MOE_OK, 0)
+    ro, rl, ob, lb = ragged_ref(q, kv[..., :128], kp, kv[..., 128:], [nq], [n], False, dtype)
+    ob = ob + added_up(n, ragged_ref(q, kv[..., :128], kp, kv[..., 128:].abs(), [nq], [n], False, dtype)[0])
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_ragged_rising_scores_in_both_types(dtype):
+    # the reference maximum moves in every tile, up to weights near the largest that fit the type
+    n = 640
+    q, kv, kp = randn(n, 1, 192, seed=1, dtype=dtype) * 0.1, randn(n, 1, 256, seed=2, dtype=dtype), randn(n, 64, seed=3, dtype=dtype) * 0.1
+    for step in (0.02, 0.6, 4.0):
+        kp[:, 0], q[..., 128] = torch.arange(n).to(dtype), step
+        kvd = kv.to(DEV)
+        o, lse = moe.mla_attn_ragged(q.to(DEV), kvd[..., :128], kp.to(DEV), kvd[..., 128:], offsets([n]), offsets([n]), n,
+                                     SCALE, want_lse=True)
+        ro, rl, ob, lb = ragged_ref(q, kv[..., :128], kp, kv[..., 128:], [n], [n], True, dtype)
+        check(o, ro, ob, "out")
+        check(lse, rl, lb, "lse")
 
 
 def test_ragged_strides_and_output_view():
