@@ -62,7 +62,6 @@ constexpr int kTmemS = 256;                      // 2 x 64 columns
 // rescaled a few times per item instead of once per tile. (Differences are compared: at
 // references where 8 is less than the spacing of fp32 a sum would round past it.)
 constexpr float kLag = 8.0f;
-constexpr int kNoPage = -0x7fffffff - 1;
 // Fewest key tiles a CTA is given: one, unless every item has an even number of them. Then
 // two make half as many partial sums, and still no CTA has pieces of two items, which would
 // cost it two results and two sets of queries (two sequences of 4,000 tokens, 63 tiles:
@@ -173,12 +172,12 @@ struct Walk {
 };
 
 // Walks the same part key tile by key tile and reads the page table one tile ahead of
-// its user: page[i], row[i] of the boxes of the present tile (kNoPage past the last key).
+// its user: page[i], row[i] of the boxes of the present tile, of which `boxes` hold keys.
 struct Cursor {
     Walk w;
     const int32_t *tab;
     int j, n, key, at, end;
-    int page[kMaxSubs], row[kMaxSubs];
+    int boxes, page[kMaxSubs], row[kMaxSubs];
 
     __device__ void start(const PagedArgs &a, const Shared &sh) {
         w.start(a, sh);
@@ -205,7 +204,7 @@ struct Cursor {
         for (int i = 0; i < kMaxSubs; ++i) {
             if (i * a.box_rows >= kKeys) break;
             row[i] = at;
-            page[i] = key < end ? *tab : kNoPage;
+            if (key < end) page[i] = *tab, boxes = i + 1;
             key += a.box_rows;
             at += a.box_rows;
             if (at == a.page_size) at = 0, ++tab;
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // A box past the last key repeats the tile's first: its scores are masked and
                     // its values cleared, whereas a box outside the cache would cost a request
                     // per row, all CTAs' at one place. A page that is not one reads zeros.
-                    const bool none = cur.page[i] == kNoPage;
+                    const bool none = i > 0 && i >= cur.boxes;
                     const bool bad = !none && static_cast<uint32_t>(cur.page[i]) >= static_cast<uint32_t>(a.num_pages);
                     if (bad) record_error(a.err, ERR_BAD_INDEX);
                     z[i] = none ? z[0] : bad ? static_cast<int>(a.num_pages) : cur.page[i];

@@ -485,6 +485,17 @@ def test_paged_bad_indices_are_reported_and_skipped():
     assert error_word() == (_lib.MOE_OK, 0)
 
 
+@pytest.mark.parametrize("entry", [9, 0])
+@pytest.mark.parametrize("page", [-(2 ** 31), -1, 2 ** 31 - 1])
+def test_paged_extreme_page_entries_are_reported(entry, page):
+    q, cache, table, ctx_t = paged_inputs([100, 100], [1, 1], 64, 8, seed=5)
+    good, _ = run_paged(q, cache, table, ctx_t, [1, 1])
+    table[1, entry] = page
+    o, _ = run_paged(q, cache, table, ctx_t, [1, 1])
+    assert error_word() == (_lib.MOE_ERR_INDEX, 0x80)
+    assert torch.equal(o[0], good[0])
+
+
 def test_paged_in_a_graph_follows_new_lengths():
     ctx, n = [90, 700], [1, 1]
     q, cache, table, ctx_t = paged_inputs([200, 800], n, 64, 64, seed=6)
