@@ -340,7 +340,8 @@ size_t mla_paged_workspace_bytes(void);
  * table   [B, max_pages] int32 (row stride table_st): the pages of sequence b in order
  * ctx     [B] int32: tokens of the sequence in the cache, the new ones included
  * out     [Tq, H, 512] (o_st, o_sh); lse [Tq, H] fp32 natural log-sum-exp, or NULL
- * 1 <= H <= 128; B <= 8192. Cache rows past a sequence's end may hold anything; a row
+ * 1 <= H <= 128; B <= 8192; rows of q that no sequence holds get no result, and with
+ * B = 0 there may be none. Cache rows past a sequence's end may hold anything; a row
  * that is some query's key is finite. Results do not depend on other sequences of the
  * batch beyond the grouping of the fp32 sums; repeated calls give the same bits. */
 int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const void *cache, int64_t page_st,
@@ -359,6 +360,7 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
  * out     [Tq, H, 128] (o_st, o_sh); lse [Tq, H] fp32 natural log-sum-exp, or NULL
  * max_q   at least the longest sequence's queries (a longer sequence
  *         is reported as an index error and skipped). 1 <= H <= 1024; B <= 65535.
+ * Rows of q that no sequence holds get no result; with B = 0 there may be none.
  * Rows outside a sequence do not reach its results, whatever they hold; a row that is
  * some query's key is finite. */
 int mla_attn_ragged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const void *k_nope, int64_t kn_st,

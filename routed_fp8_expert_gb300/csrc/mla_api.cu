@@ -88,6 +88,12 @@ int tensor_map(CUtensorMap *m, const void *p, int dtype, int rank, const int64_t
     return MOE_OK;
 }
 
+// (the offsets on the device say which rows the sequences hold; without any, no row is)
+int sequences(int B, int64_t Tq) {
+    if (B == 0) return fail(MOE_ERR_ARG, "B=0 sequences for Tq=%lld rows", static_cast<long long>(Tq));
+    return MOE_OK;
+}
+
 int proj_sizes(int T, int H, int K, int N) {
     MLA_CHECK(range(H, 1, 1024, "H"));
     if (K < 8 || K > 8192 || K % 8) return fail(MOE_ERR_UNSUPPORTED, "K=%d must be a multiple of 8 in [8, 8192]", K);
@@ -225,7 +231,8 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
     if (page_size <= 0 || page_size % 8 || page_size > (1 << 20))
         return fail(MOE_ERR_UNSUPPORTED, "page_size=%d must be a multiple of 8 in [8, 2^20]", page_size);
     MLA_CHECK(range(num_pages, 1, (int64_t{1} << 31) - 2, "num_pages"));
-    if (B == 0 || Tq == 0) return MOE_OK;
+    if (Tq == 0) return MOE_OK;
+    MLA_CHECK(sequences(B, Tq));
     MLA_CHECK(range(max_pages, 0, (int64_t{1} << 31) - 1, "max_pages"));
     MLA_CHECK(ptr(q, "q"));
     MLA_CHECK(stride(q_st, 8, "q_st"));
@@ -301,7 +308,8 @@ int mla_attn_ragged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const
     MLA_CHECK(count(Tq, "Tq"));
     MLA_CHECK(count(Tk, "Tk"));
     MLA_CHECK(count(max_q, "max_q"));
-    if (B == 0 || Tq == 0 || max_q == 0) return MOE_OK;
+    if (Tq == 0) return MOE_OK;
+    MLA_CHECK(sequences(B, Tq));
     MLA_CHECK(ptr(q, "q"));
     MLA_CHECK(stride(q_st, 8, "q_st"));
     MLA_CHECK(stride(q_sh, 8, "q_sh"));

@@ -443,7 +443,8 @@ cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &kn, const CUtensor
 
 cudaError_t launch_ragged(const CUtensorMap &q, const CUtensorMap &k_nope, const CUtensorMap &k_pe,
                           const CUtensorMap &v, const RaggedArgs &a, bool bf16, cudaStream_t stream) {
-    const int64_t tiles = (a.max_q + kQRows - 1) / kQRows, slots = a.Tq / kQRows + a.B;
+    // (max_q = 0: one tile, which reports the sequences that have queries all the same)
+    const int64_t tiles = a.max_q > 0 ? (a.max_q + kQRows - 1) / kQRows : 1, slots = a.Tq / kQRows + a.B;
     if (tiles * a.B >= kSlotRatio * slots) {
         const dim3 grid(static_cast<unsigned>(slots), a.H);
         return bf16 ? launch_t<__nv_bfloat16, true>(q, k_nope, k_pe, v, a, grid, stream)

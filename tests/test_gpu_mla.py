@@ -660,6 +660,17 @@ def test_ragged_bad_offsets_are_reported_and_skipped():
         assert (out == 3.0).all()
 
 
+def test_ragged_bound_of_zero_reports_queries():
+    q, kv, kp = randn(20, 3, 192).to(DEV), randn(20, 3, 256).to(DEV), randn(20, 64).to(DEV)
+    for lens, word in (([0, 20, 0], (_lib.MOE_ERR_INDEX, 0x80)), ([0, 0, 0], (_lib.MOE_OK, 0))):
+        out = torch.full((20, 3, 128), 3.0, dtype=BF16, device=DEV)
+        moe.mla_attn_ragged(q, kv[..., :128], kp, kv[..., 128:], offsets(lens), offsets(lens), 0, SCALE, out=out)
+        assert error_word() == word
+        assert (out == 3.0).all()
+    with pytest.raises(moe.MoeError, match="B=0"):
+        moe.mla_attn_ragged(q, kv[..., :128], kp, kv[..., 128:], offsets([]), offsets([]), 20, SCALE)
+
+
 @pytest.mark.parametrize("nq", [
     [9], [700, 3, 0, 256, 512, 1, 257], [255, 1, 0, 0, 300] * 8, [i % 4 for i in range(1100)], [0] * 40 + [513] + [0] * 40,
 ])

@@ -92,6 +92,7 @@ ARG, UNS = _lib.MOE_ERR_ARG, _lib.MOE_ERR_UNSUPPORTED
     ("mla_attn_ragged", RAGGED, dict(v=ODD), ARG), ("mla_attn_ragged", RAGGED, dict(kp_st=60), ARG),
     ("mla_attn_ragged", RAGGED, dict(cu_k=None), ARG), ("mla_attn_ragged", RAGGED, dict(o_st=64), ARG),
     ("mla_attn_ragged", RAGGED, dict(scale=-1.0), ARG), ("mla_attn_ragged", RAGGED, dict(q_st=1 << 40), ARG),
+    ("mla_attn_paged", PAGED, dict(B=0, cu_q=P), ARG), ("mla_attn_ragged", RAGGED, dict(B=0), ARG),   # rows, but no sequence
     ("mla_head_proj", PROJ, dict(dtype=9), ARG), ("mla_head_proj", PROJ, dict(shared=2), ARG),
     ("mla_head_proj", PROJ, dict(w_kn=-1), ARG), ("mla_head_proj", PROJ, dict(K=12), UNS),
     ("mla_head_proj", PROJ, dict(K=0), UNS), ("mla_head_proj", PROJ, dict(N=4), UNS),
