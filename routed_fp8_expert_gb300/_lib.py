@@ -361,7 +361,9 @@ def test_wait_timeout(limit_ns: int, device=None):
 
 
 def check_device_error(device=None):
-    """Synchronise and read/clear the device error word; raises MoeError on a timeout."""
+    """Synchronise and read/clear the error word of `device` (None: the current one); raises
+    MoeError on a timeout or a bad index."""
     detail = ctypes.c_uint32(0)
-    _check(load().moe_check_device_error(_stream(device), ctypes.byref(detail)))
+    with torch.cuda.device(device):
+        _check(load().moe_check_device_error(_stream(device), ctypes.byref(detail)))
     return detail.value

@@ -3,7 +3,7 @@
 Argument marshalling only, as in _lib: tensors on the CUDA device, bf16 or fp16, the
 innermost dimension contiguous; any other stride goes to the kernels as it is (views
 of wider projections and of multi-layer caches need no copy). Outputs are allocated
-when not given; the current stream of the inputs' device is used.
+when not given; a call runs on the inputs' device, on its current stream.
 """
 from __future__ import annotations
 
@@ -22,6 +22,17 @@ _LAYOUTS = {"interleaved": 0, "half": 1}
 
 # the raw handle: building a torch.cuda.Stream object costs more than a small launch
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _enqueue(dev, fn, *args):
+    """Make the C call on device `dev`: the library asks the current device for its SMs, its
+    error word and its launch, which has to be the device of the tensors and the stream."""
+    if _current_device() == dev:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args))
 
 
 def _bad(msg):
@@ -164,8 +175,8 @@ def mla_rope_append(q_pe, kv, positions, plan: RopePlan, gamma=None, eps: float 
         _bad("cache or kv_out is given without kv")
     pp = _vec("positions", positions, T, torch.int32, dev)
     fp = _vec("plan.freq", plan.freq, dim // 2, torch.int64, dev)
-    _check(load().mla_rope_append(*qa, *qo, *ka, gp, eps, *ko, *ca, pages, page, sp, pp, fp, plan.amplitude, plan.layout,
-                                  T, H, dim, latent, code, _raw_stream(dev)))
+    _enqueue(dev, load().mla_rope_append, *qa, *qo, *ka, gp, eps, *ko, *ca, pages, page, sp, pp, fp, plan.amplitude,
+             plan.layout, T, H, dim, latent, code, _raw_stream(dev))
     return q_out, kv_out
 
 
@@ -196,12 +207,13 @@ def mla_attn_paged(q, cache, block_table, ctx_lens, scale: float, cu_q=None, out
         ws = mla_paged_workspace(q.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         _bad("ws must be contiguous and on the call's device")
-    _check(load().mla_attn_paged(
-        *_ten("q", q, Tq, H, width, ty, dev), Tq, *_ten("cache", cache, pages, page, width, ty, dev), pages, page, tp,
-        t_st if B > 1 else max_pages, max_pages, _vec("ctx_lens", ctx_lens, B, torch.int32, dev),
+    _enqueue(
+        dev, load().mla_attn_paged, *_ten("q", q, Tq, H, width, ty, dev), Tq,
+        *_ten("cache", cache, pages, page, width, ty, dev), pages, page, tp, t_st if B > 1 else max_pages, max_pages,
+        _vec("ctx_lens", ctx_lens, B, torch.int32, dev),
         None if cu_q is None else _vec("cu_q", cu_q, B + 1, torch.int32, dev), B, H, scale, code,
         *_ten("out", out, Tq, H, MLA_LATENT, ty, dev), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
-        _raw_stream(dev)))
+        _raw_stream(dev))
     return (out, lse) if want_lse else out
 
 
@@ -220,12 +232,12 @@ def mla_attn_ragged(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, scale: float, ca
     if out is None:
         out = torch.empty((Tq, H, MLA_V), dtype=ty, device=q.device)
     lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device) if want_lse else None
-    _check(load().mla_attn_ragged(
-        *_ten("q", q, Tq, H, MLA_NOPE + MLA_ROPE, ty, dev), Tq, *_ten("k_nope", k_nope, Tk, H, MLA_NOPE, ty, dev),
-        *_mat("k_pe", k_pe, Tk, MLA_ROPE, ty, dev), *_ten("v", v, Tk, H, MLA_V, ty, dev), Tk,
-        _vec("cu_q", cu_q, B + 1, torch.int32, dev), _vec("cu_k", cu_k, B + 1, torch.int32, dev), B, max_q, H, scale,
-        1 if causal else 0, code, *_ten("out", out, Tq, H, MLA_V, ty, dev), None if lse is None else lse.data_ptr(),
-        _raw_stream(dev)))
+    _enqueue(
+        dev, load().mla_attn_ragged, *_ten("q", q, Tq, H, MLA_NOPE + MLA_ROPE, ty, dev), Tq,
+        *_ten("k_nope", k_nope, Tk, H, MLA_NOPE, ty, dev), *_mat("k_pe", k_pe, Tk, MLA_ROPE, ty, dev),
+        *_ten("v", v, Tk, H, MLA_V, ty, dev), Tk, _vec("cu_q", cu_q, B + 1, torch.int32, dev),
+        _vec("cu_k", cu_k, B + 1, torch.int32, dev), B, max_q, H, scale, 1 if causal else 0, code,
+        *_ten("out", out, Tq, H, MLA_V, ty, dev), None if lse is None else lse.data_ptr(), _raw_stream(dev))
     return (out, lse) if want_lse else out
 
 
@@ -242,6 +254,6 @@ def mla_head_proj(x, w, w_kn: bool = False, out=None):
     if out is None:
         out = torch.empty((T, H, N), dtype=ty, device=x.device)
     wa = _ten("w", w, H, K, N, ty, dev) if w_kn else _ten("w", w, H, N, K, ty, dev)
-    _check(load().mla_head_proj(*_ten("x", x, T, xh, K, ty, dev), 1 if xh == 1 else 0, *wa, 1 if w_kn else 0, T, H, K, N,
-                                code, *_ten("out", out, T, H, N, ty, dev), _raw_stream(dev)))
+    _enqueue(dev, load().mla_head_proj, *_ten("x", x, T, xh, K, ty, dev), 1 if xh == 1 else 0, *wa, 1 if w_kn else 0, T,
+             H, K, N, code, *_ten("out", out, T, H, N, ty, dev), _raw_stream(dev))
     return out

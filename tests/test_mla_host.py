@@ -1,16 +1,18 @@
 """Latent attention on the host: rotary frequencies and the refusals of every call.
 No GPU: bad arguments are turned away before anything is enqueued."""
+import contextlib
 import ctypes
 import math
 import os
 import re
+import types
 
 import pytest
 import torch
 
 import routed_fp8_expert_gb300 as moe
 from _mla_ref import rope_frequencies
-from routed_fp8_expert_gb300 import _lib, build
+from routed_fp8_expert_gb300 import _lib, build, mla
 
 P = ctypes.c_void_p(0x1000)
 ODD = ctypes.c_void_p(0x1008)
@@ -132,6 +134,58 @@ def test_binding_wants_cuda_tensors():
     x = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         moe.mla_head_proj(x, torch.zeros(4, 8, 128, dtype=torch.bfloat16))
+
+
+class On:
+    """A CPU tensor that says it lies on a CUDA device."""
+
+    def __init__(self, device, t):
+        self.t, self.index = t, device
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("dev", [0, 1])
+def test_binding_calls_on_the_device_of_the_tensors(monkeypatch, dev):
+    # current device 0: a fake library notes the device that is current when it is called
+    current, seen = [0], []
+
+    @contextlib.contextmanager
+    def device(i):
+        before, current[0] = current[0], i
+        yield
+        current[0] = before
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: seen.append((name, current[0], a[-1])) or _lib.MOE_OK
+
+    monkeypatch.setattr(mla, "load", Lib)
+    monkeypatch.setattr(mla, "_raw_stream", lambda i: 100 + i)
+    monkeypatch.setattr(mla, "_current_device", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+
+    def z(*shape, dtype=torch.bfloat16):
+        return On(dev, torch.zeros(*shape, dtype=dtype))
+
+    i32 = torch.int32
+    plan = types.SimpleNamespace(freq=z(32, dtype=torch.int64), dim=64, layout=0, amplitude=1.0)
+    moe.mla_rope_append(z(4, 8, 64), z(4, 576), z(4, dtype=i32), plan, q_out=z(4, 8, 64), kv_out=z(4, 576))
+    moe.mla_attn_paged(z(2, 8, 576), z(3, 8, 576), z(2, 1, dtype=i32), z(2, dtype=i32), 1.0, out=z(2, 8, 512),
+                       ws=z(64, dtype=torch.uint8))
+    moe.mla_attn_ragged(z(4, 8, 192), z(4, 8, 128), z(4, 64), z(4, 8, 128), z(2, dtype=i32), z(2, dtype=i32), 4, 1.0,
+                        out=z(4, 8, 128))
+    moe.mla_head_proj(z(4, 8, 128), z(8, 16, 128), out=z(4, 8, 16))
+    names = ("mla_rope_append", "mla_attn_paged", "mla_attn_ragged", "mla_head_proj")
+    assert seen == [(n, dev, 100 + dev) for n in names] and current == [0]
+    monkeypatch.setattr(_lib, "load", Lib)
+    monkeypatch.setattr(_lib, "_stream", lambda i: 100 + i)
+    moe.check_device_error(dev)                              # the error word of that device
+    assert seen[-1][:2] == ("moe_check_device_error", dev) and current == [0]
 
 
 def test_paged_exchanges_of_a_single_tile_are_separated_by_barriers():
