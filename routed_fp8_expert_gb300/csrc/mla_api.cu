@@ -240,7 +240,7 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
     MLA_CHECK(ptr(cache, "cache"));
     MLA_CHECK(stride(row_st, kMlaWidth, "row_st"));
     MLA_CHECK(stride(page_st, kMlaWidth, "page_st"));
-    MLA_CHECK(ptr(table, "table", 4));
+    if (max_pages > 0) MLA_CHECK(ptr(table, "table", 4));   // (without pages no sequence has keys)
     if (table_st < max_pages && B > 1)
         return fail(MOE_ERR_ARG, "table_st=%lld is below max_pages=%d", static_cast<long long>(table_st), max_pages);
     MLA_CHECK(ptr(ctx, "ctx", 4));

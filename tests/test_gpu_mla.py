@@ -485,6 +485,17 @@ def test_paged_bad_indices_are_reported_and_skipped():
     assert error_word() == (_lib.MOE_OK, 0)
 
 
+def test_paged_without_any_page():
+    q, cache = randn(3, 5, 576, seed=1).to(DEV), randn(2, 16, 576, seed=2).to(DEV)
+    table, ctx = torch.zeros(3, 0, dtype=torch.int32, device=DEV), torch.zeros(3, dtype=torch.int32, device=DEV)
+    out = torch.full((3, 5, 512), 4.0, dtype=BF16, device=DEV)
+    o, lse = moe.mla_attn_paged(q, cache, table, ctx, SCALE, out=out, want_lse=True)
+    assert error_word() == (_lib.MOE_OK, 0) and (o == 0).all() and (lse == -math.inf).all()
+    ctx[1] = 1                                               # a key, but no page
+    moe.mla_attn_paged(q, cache, table, ctx, SCALE)
+    assert error_word() == (_lib.MOE_ERR_INDEX, 0x80)
+
+
 @pytest.mark.parametrize("entry", [9, 0])
 @pytest.mark.parametrize("page", [-(2 ** 31), -1, 2 ** 31 - 1])
 def test_paged_extreme_page_entries_are_reported(entry, page):

@@ -121,6 +121,13 @@ def test_head_proj_form(lib, T, H, K, N, shared, form):
     assert lib.mla_head_proj_form(T, H, K, N, shared) == form
 
 
+def test_an_empty_page_table_needs_no_address(lib):
+    assert lib.mla_attn_paged(*dict(PAGED, table=None, max_pages=0, ctx=None).values()) == ARG
+    assert b"ctx is NULL" in lib.moe_last_error_string()     # the check after the table's
+    assert lib.mla_attn_paged(*dict(PAGED, table=None, max_pages=1, ctx=None).values()) == ARG
+    assert b"table is NULL" in lib.moe_last_error_string()
+
+
 def test_nothing_to_do(lib):
     assert lib.mla_rope_append(*dict(ROPE, T=0, q=None, positions=None).values()) == _lib.MOE_OK
     assert lib.mla_attn_paged(*dict(PAGED, B=0, Tq=0, q=None, ctx=None).values()) == _lib.MOE_OK
