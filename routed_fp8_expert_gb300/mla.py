@@ -170,6 +170,8 @@ def mla_rope_append(q_pe, kv, positions, plan: RopePlan, gamma=None, eps: float 
                 _bad("cache is given without slots")
             pages, page, _ = _dims("cache", cache, 3)
             ca = _ten("cache", cache, pages, page, width, ty, dev)
+            if pages == 0:   # no address, which would mean no cache: any will do, since no slot lies in it
+                ca = (kv.data_ptr(), *ca[1:])
             sp = _vec("slots", slots, T, torch.int32, dev)
     elif cache is not None or kv_out is not None:
         _bad("cache or kv_out is given without kv")

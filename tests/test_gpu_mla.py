@@ -187,6 +187,22 @@ def test_rope_bad_slot_is_skipped_and_reported():
     assert (flat[3] != 0).any() and flat.abs().sum() == flat[3].abs().sum()
 
 
+def test_rope_with_a_cache_of_no_pages():
+    # no slot lies in it: tokens that are not cached are fine, any other is reported
+    plan = moe.rope_plan(64, device=DEV)
+    kv, cache = randn(3, 576, seed=1).to(DEV), torch.zeros(0, 8, 576, dtype=BF16, device=DEV)
+    pos = torch.arange(3, dtype=torch.int32, device=DEV)
+    _, want = moe.mla_rope_append(None, kv, pos, plan)
+    before = kv.clone()
+    for slots, word in (([-1, -1, -1], (_lib.MOE_OK, 0)), ([-1, 0, -1], (_lib.MOE_ERR_INDEX, 0x80))):
+        slots = torch.tensor(slots, dtype=torch.int32, device=DEV)
+        _, rows = moe.mla_rope_append(None, kv, pos, plan, cache=cache, slots=slots, kv_out=torch.empty_like(kv))
+        assert error_word() == word
+        assert torch.equal(rows, want) and torch.equal(kv, before)
+        moe.mla_rope_append(None, kv, pos, plan, cache=cache, slots=slots)
+        assert error_word() == word and torch.equal(kv, before)
+
+
 def test_rope_of_a_strided_multi_layer_cache():
     layers, page = 3, 16
     plan = moe.rope_plan(64, device=DEV)
