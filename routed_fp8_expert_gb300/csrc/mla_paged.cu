@@ -62,11 +62,17 @@ constexpr int kTmemS = 256;                      // 2 x 64 columns
 // rescaled a few times per item instead of once per tile. (Differences are compared: at
 // references where 8 is less than the spacing of fp32 a sum would round past it.)
 constexpr float kLag = 8.0f;
-// Fewest key tiles a CTA is given: one, unless every item has an even number of them. Then
-// two make half as many partial sums, and still no CTA has pieces of two items, which would
-// cost it two results and two sets of queries (two sequences of 4,000 tokens, 63 tiles:
-// 19.3 us with two tiles, 16.4 with one; 60 of 128: 12.6 and 16.4; 8 of 1,000: 17.4 and
-// 18.7; one of 1,000: 13.7 and 13.1).
+// Fewest key tiles a CTA is given: one, or, where that cuts no CTA's part between two items,
+// two, which make half as many partial sums. A CTA with pieces of two items has two results
+// and two sets of queries.
+// - No more tiles than CTAs: two if every item has an even number of them (one sequence of
+//   960 tokens and 128 heads, two items of 15 tiles: with two 16.2 us, with one 12.9; two
+//   sequences of 4,000, 63 tiles: 19.3 and 16.4; 60 of 128: 12.6 and 16.4; 8 of 1,000: 17.4
+//   and 18.7; one of 1,000: 13.7 and 13.1).
+// - Up to twice as many: one would leave some CTAs two all the same. Two if every sequence's
+//   items together have an even number (one of 8,000 tokens and 128 heads, two items of 125
+//   tiles: with two 19.2 us, with one 21.2; sequences of 100, 700 and 5,000 tokens in one
+//   call: 21.2 and 19.5).
 constexpr int kEvenTiles = 2;
 
 static_assert(kQBytes >= 8192 * 8, "the start-up scan keeps one 8-byte prefix per sequence in the query buffer");
@@ -234,17 +240,21 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t base = 0;
-    bool odd = false;
+    bool odd_items = false, odd_sums = false;   // of an item; of a sequence's items together
     if (tid == 0) sh.start_b = 0, sh.start_rt = 0, sh.start_off = 0, sh.start = Seq{0, 0, 0};   // a CTA without a part
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
         Seq s{0, 0, 0};
         if (b < a.B) s = read_seq(a, b, blockIdx.x == 0);
         int64_t u = 0;
+        int any = 0;   // the items' lengths
         const int rts = row_tiles(s, a.H);
         // few row tiles: one thread per sequence; many: the warp takes them together
         if (rts <= 8)
-            for (int r = 0; r < rts; ++r) u += units_of(tile_keys(a, s, r));
+            for (int r = 0; r < rts; ++r) {
+                const int n = units_of(tile_keys(a, s, r));
+                u += n, any |= n;
+            }
         unsigned many = __ballot_sync(0xffffffffu, rts > 8);
         while (many) {
             const int src = __ffs(many) - 1;
@@ -255,14 +265,17 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
             o.ctx = __shfl_sync(0xffffffffu, s.ctx, src);
             const int orts = __shfl_sync(0xffffffffu, rts, src);
             int64_t v = 0;
-            for (int r = lane; r < orts; r += 32) v += units_of(tile_keys(a, o, r));
+            for (int r = lane; r < orts; r += 32) {
+                const int n = units_of(tile_keys(a, o, r));
+                v += n, any |= n;
+            }
 #pragma unroll
             for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
             if (lane == src) u = v;
         }
         const int64_t inc = warp_scan(u, lane);
         if (lane == 31) sh.warp_sum[warp] = inc;
-        odd |= __syncthreads_or(u & 1);
+        odd_items |= __syncthreads_or(any & 1);
         int64_t before = base, all = 0;
 #pragma unroll 1
         for (int w = 0; w < min(kThreads, a.B - b0 + 31) / 32; ++w) {   // (short code: it runs once)
@@ -271,8 +284,9 @@ __device__ void plan(const PagedArgs &a, Shared &sh, int64_t *prefix) {
         }
         if (b < a.B) prefix[b] = before + inc - u;
         base += all;
-        __syncthreads();
+        odd_sums |= __syncthreads_or(u & 1);
     }
+    const bool odd = base <= gridDim.x ? odd_items : odd_sums;
     const int64_t most = odd ? base : base / kEvenTiles;
     const unsigned parts = most < 1 ? 1u : most < gridDim.x ? static_cast<unsigned>(most) : gridDim.x;
     int64_t each;

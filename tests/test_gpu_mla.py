@@ -430,6 +430,24 @@ def test_paged_single_tile_segments_repeat(ctx, H):
     assert error_word() == (_lib.MOE_OK, 0)
 
 
+@pytest.mark.parametrize("H,n,ctx,joins", [
+    (128, 1, [129], [[0, 2], [3, 5]]),                       # two items of three tiles: one tile a CTA
+    (128, 1, [256], [[0, 1], [2, 3]]),                       # of four: two
+    (64, 1, [129, 60], [[0, 2]]), (64, 1, [128, 256], [[1, 2]]), (16, 4, [65], []), (64, 2, [130], [[0, 2], [3, 5]]),
+])
+def test_paged_cuts_items_of_odd_tiles_singly(H, n, ctx, joins):
+    # the list of shared items that the first kernel leaves to the join: (first, last) CTA of each
+    q, cache, table, ctx_t = paged_inputs(ctx, [n] * len(ctx), H, 64, seed=H)
+    ws = moe.mla_paged_workspace(DEV)
+    o, lse = run_paged(q, cache, table, ctx_t, [n] * len(ctx), ws=ws)
+    ro, rl, ob, lb = paged_ref(q, cache, table, ctx_t, [n] * len(ctx), BF16)
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    entries = ws[-16 * ctas:].view(torch.int32).view(ctas, 4).tolist()
+    assert [[c, e[3]] for c, e in enumerate(entries) if e[2] > 0] == joins
+
+
 def test_paged_views_and_strides():
     ctx, n, H = [150, 90], [1, 1], 8
     q, cache, table, ctx_t = paged_inputs(ctx, n, H, 32, seed=11)
