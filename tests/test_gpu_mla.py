@@ -462,6 +462,51 @@ def test_paged_views_and_strides():
     assert torch.equal(got, base) and torch.equal(lse, lse0) and (out[..., 512:] == 5.0).all()
 
 
+def check_paged_sample(q, cache, table, ctx, n, o, lse, rows, dtype=BF16):
+    """The given (sequence, query) rows of a call against their 64-bit form: q [Tq, H, 576]."""
+    page, start = cache.shape[1], [0]
+    for x in n:
+        start.append(start[-1] + x)
+    for b, i in rows:
+        c = int(ctx[b])
+        keys = torch.cat([cache[p] for p in table[b, :(c + page - 1) // page].tolist()])[:c]
+        t, H = start[b] + i, q.shape[1]
+        ro, rl, ob, lb = attention(q[t], keys, keys[:, :512], [max(0, c - n[b] + i + 1)] * H, SCALE, dtype)
+        check(o[t], ro, ob, f"out of query {i} of sequence {b}")
+        check(lse[t], rl, lb, f"lse of query {i} of sequence {b}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("H,ctx,n", [
+    (64, [700, 6001, 300, 9000, 33, 4100], [300, 1, 257, 1, 1, 4]),      # prompts' chunks beside single tokens
+    (16, [513, 20000, 2000, 1, 77], [513, 1, 70, 1, 5]),
+    (128, [9000, 513, 64], [1, 200, 1]), (100, [3000, 800], [2, 333]),
+])
+def test_paged_chunks_beside_single_tokens(H, ctx, n, dtype):
+    q, cache, table, ctx_t = paged_inputs(ctx, n, H, 64, seed=sum(n) + H, dtype=dtype, junk=math.nan)
+    o, lse = run_paged(q, cache, table, ctx_t, n)
+    assert error_word() == (_lib.MOE_OK, 0)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    rows = sorted({(b, i) for b, x in enumerate(n) for i in (0, 1, x // 2, x - 2, x - 1) if 0 <= i < x})
+    check_paged_sample(q, cache, table, ctx_t, n, o, lse, rows, dtype)
+    o2, lse2 = run_paged(q, cache, table, ctx_t, n)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)     # the same bits again
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("H,n,ctx", [
+    (128, 1, [12000, 700, 9001, 64, 3000]), (128, 1, [4000 + 61 * i for i in range(40)]), (96, 3, [8000, 5000, 7001]),
+    (64, 4, [6000 + 77 * i for i in range(12)]), (128, 2, [20000]),
+])
+def test_paged_many_row_tiles_over_long_contexts(H, n, ctx, dtype):
+    q, cache, table, ctx_t = paged_inputs(ctx, [n] * len(ctx), H, 32, seed=len(ctx) + H, dtype=dtype, junk=math.inf)
+    o, lse = run_paged(q, cache, table, ctx_t, [n] * len(ctx))
+    assert error_word() == (_lib.MOE_OK, 0)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    check_paged_sample(q, cache, table, ctx_t, [n] * len(ctx), o, lse,
+                       sorted({(b, i) for b in (0, len(ctx) // 2, len(ctx) - 1) for i in (0, n - 1)}), dtype)
+
+
 def test_offsets_past_32_bits():
     # pages whose element offsets pass 2^32: appended to, then read
     page, pages = 64, 120_000
@@ -678,6 +723,22 @@ def test_ragged_rising_scores_in_both_types(dtype):
         ro, rl, ob, lb = ragged_ref(q, kv[..., :128], kp, kv[..., 128:], [n], [n], True, dtype)
         check(o, ro, ob, "out")
         check(lse, rl, lb, "lse")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_ragged_long_uneven_sequences(dtype, causal):
+    # long, short, after a prefix, queries that see nothing, more queries than keys
+    nq, nk, H = [1900, 3, 700, 0, 513, 1], [1900, 2500, 1217, 300, 100, 4097], 2
+    q = randn(sum(nq), H, 192, seed=1, dtype=dtype)
+    kv, kp = randn(sum(nk), H, 256, seed=2, dtype=dtype), randn(sum(nk), 64, seed=3, dtype=dtype)
+    kvd = kv.to(DEV)
+    o, lse = moe.mla_attn_ragged(q.to(DEV), kvd[..., :128], kp.to(DEV), kvd[..., 128:], offsets(nq), offsets(nk), max(nq),
+                                 SCALE, causal=causal, want_lse=True)
+    assert error_word() == (_lib.MOE_OK, 0)
+    ro, rl, ob, lb = ragged_ref(q, kv[..., :128], kp, kv[..., 128:], nq, nk, causal, dtype)
+    check(o, ro, ob, "out")
+    check(lse, rl, lb, "lse")
 
 
 def test_ragged_strides_and_output_view():
