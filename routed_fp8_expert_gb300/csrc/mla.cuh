@@ -98,16 +98,9 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
                  : "r"(taddr));
 }
 
-// 16 lanes x 64 columns in the 16x256b shape: thread t gets, for every 8-column group
-// g, columns 8g + 2(t % 4) + {0, 1} of lane t / 4 (r[4g], r[4g + 1]) and of lane
-// t / 4 + 8 (r[4g + 2], r[4g + 3]).
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 " MLA_LIST32 ", [%32];"
-                 : MLA_R8(0), MLA_R8(8), MLA_R8(16), MLA_R8(24)
-                 : "r"(taddr));
-}
-
-// 16 lanes x 32 columns in the 16x256b shape (tmem_ld_16x64, four 8-column groups).
+// 16 lanes x 32 columns in the 16x256b shape: thread t gets, for every 8-column group g,
+// columns 8g + 2(t % 4) + {0, 1} of lane t / 4 (r[4g], r[4g + 1]) and of lane t / 4 + 8
+// (r[4g + 2], r[4g + 3]).
 __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
@@ -292,31 +285,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
         : "=r"(ok)
         : "r"(bar), "r"(parity)
         : "memory");
-    return ok != 0;
-}
-
-// Work stealing: asks for a CTA of this launch that has not started yet, to run its work
-// here instead. The 16-byte answer counts on `bar` like a copy. After an answer
-// without a CTA no further request may be made.
-__device__ __forceinline__ void clc_request(uint32_t answer, uint32_t bar) {
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
-        "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ bool clc_answer(uint32_t answer, int &x, int &y, int &z) {
-    uint32_t ok, cx, cy, cz;
-    asm volatile(
-        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
-        "ld.shared.b128 h, [%4];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t"
-        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, h;\n\t}"
-        : "=r"(ok), "=r"(cx), "=r"(cy), "=r"(cz)
-        : "r"(answer)
-        : "memory");
-    x = cx, y = cy, z = cz;
     return ok != 0;
 }
 

@@ -232,18 +232,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // each CTA holds half of the tokens' rows, one of the two weight blocks and the results
 // of its rows. A CTA's chunk of x then feeds MMAs of twice the width, so that its ring of
 // five covers the loads' latency (1,700 cycles) at the tensor rate.
-struct PairShared {
-    uint64_t x_full[kXSlots], x_empty[kXSlots], w_full[kWSlots], w_empty[kWSlots], acc_full[2], acc_empty[2], mma_done;
-    uint32_t tmem;
-    int abort;
-};
-
 template <typename T, bool KN>
 __global__ void __launch_bounds__(kThreads, 1)
     head_proj_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                           const __grid_constant__ CUtensorMap map_out, const ProjArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    PairShared &sh = *reinterpret_cast<PairShared *>(smem + kOffMisc);
+    Shared &sh = *reinterpret_cast<Shared *>(smem + kOffMisc);
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();

@@ -16,7 +16,8 @@ enum : uint32_t {
     ERR_WAIT_DRAIN = 1u << 4,      // draining in-flight copies / MMAs timed out
     ERR_BAD_TILE = 1u << 5,        // a schedule entry was out of range (skipped)
     ERR_WAIT_SELFTEST = 1u << 6,   // the bounded-wait self-test gave up, as it must
-    ERR_BAD_INDEX = 1u << 7,       // (bounds-checked build) an index outside its buffer (access skipped)
+    ERR_BAD_INDEX = 1u << 7,       // an index outside its buffer, access skipped (latent attention: a slot,
+                                   // page, length or offset; bounds-checked build: see below)
 };
 
 // The bounds-checked build (-DMOE_DEBUG_BOUNDS): every index that addresses a row
