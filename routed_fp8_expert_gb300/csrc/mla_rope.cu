@@ -11,11 +11,12 @@ namespace {
 // One CTA per token. With f_i the pair's frequency in turns per position,
 //   (a, b) -> amplitude * (a cos - b sin, b cos + a sin),  angle = 2 pi frac(pos * f_i).
 // The frequency is a 64-bit fixed-point fraction of a turn, so pos * f_i wraps modulo
-// one turn in integer arithmetic: at position 2^20 the phase is off by at most 2^-36
-// turns (the frequency's own rounding to 53 bits), where an fp32 product of position
-// and frequency would be off by 2^-7.
-// Its upper 32 bits, as a signed number of half turns, feed sincospi. All arithmetic is
-// fp32, rounded once when stored.
+// one turn in integer arithmetic. Its upper 32 bits, as a signed number of half turns in
+// fp32, feed sincospi: the angle is off by up to 2^-26 turns (24 bits of a number below
+// half a turn; 2^-32 for the bits that are dropped), at every position. The frequency's
+// own error, 2^-50 of it for the host's roundings in 64 bits, adds pos times that: 2^-32
+// turns at position 2^20. An fp32 product of position and frequency would be off by 2^-7
+// there. All arithmetic is fp32, rounded once when stored.
 //
 // A prompt is bound by memory, and nearly as much by the issue rate. 32 bytes per thread
 // are on their way before the angles are known; what only the key's warps need is theirs

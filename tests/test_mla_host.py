@@ -2,6 +2,7 @@
 No GPU: bad arguments are turned away before anything is enqueued."""
 import contextlib
 import ctypes
+import decimal
 import math
 import os
 import re
@@ -35,6 +36,25 @@ def test_rope_frequencies(lib, dim, base, kw):
     want = rope_frequencies(dim, base, **kw) / (2 * math.pi)
     got = torch.tensor([v / 2.0 ** 64 for v in f], dtype=torch.float64)
     assert torch.allclose(got, want, rtol=1e-14, atol=2.0 ** -63)
+
+
+@pytest.mark.parametrize("dim,base,factor", [(64, 10000.0, 1.0), (64, 50000.0, 32.0), (128, 500000.0, 8.0), (16, 1.5, 40.0)])
+def test_rope_frequencies_to_50_bits(lib, dim, base, factor):
+    # against 60 decimal digits: what the kernel's statement of the angle's error counts on
+    D = decimal.Decimal
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        two_pi = 2 * D("3.14159265358979323846264338327950288419716939937510582097494459")
+        f = (ctypes.c_uint64 * (dim // 2))()
+        assert lib.mla_rope_freqs(dim, base, factor, 4096, 32.0, 1.0, f) == _lib.MOE_OK
+        pair = lambda r: dim * (D(4096) / (two_pi * D(r))).ln() / (2 * D(base).ln())  # noqa: E731
+        low, high = max(math.floor(pair(32)), 0), min(math.ceil(pair(1)), dim - 1)
+        for i in range(dim // 2):
+            want = (-D(2 * i) / D(dim) * D(base).ln()).exp() / two_pi
+            if factor > 1:
+                ramp = min(D(1), max(D(0), D(i - low) / max(D(high - low), D("0.001"))))
+                want = want * (1 - ramp) + want / D(factor) * ramp
+            assert abs(D(f[i]) - want * 2 ** 64) <= want * 2 ** 14 + 1
 
 
 @pytest.mark.parametrize("args,code", [
