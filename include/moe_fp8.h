@@ -342,7 +342,8 @@ size_t mla_paged_workspace_bytes(void);
  * out     [Tq, H, 512] (o_st, o_sh); lse [Tq, H] fp32 natural log-sum-exp, or NULL
  * 1 <= H <= 128; B <= 8192; rows of q that no sequence holds get no result, and with
  * B = 0 there may be none. Cache rows past a sequence's end may hold anything; a row
- * that is some query's key is finite. Results do not depend on other sequences of the
+ * that is some query's key is finite (bf16: below 2^119, since a weight may stand at 2^8
+ * before the division). Results do not depend on other sequences of the
  * batch beyond the grouping of the fp32 sums; repeated calls give the same bits. */
 int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const void *cache, int64_t page_st,
                    int64_t row_st, int64_t num_pages, int page_size, const int32_t *table, int64_t table_st,
@@ -362,7 +363,7 @@ int mla_attn_paged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const 
  *         is reported as an index error and skipped). 1 <= H <= 1024; B <= 65535.
  * Rows of q that no sequence holds get no result; with B = 0 there may be none.
  * Rows outside a sequence do not reach its results, whatever they hold; a row that is
- * some query's key is finite. */
+ * some query's key is finite (bf16 values: below 2^119, as above). */
 int mla_attn_ragged(const void *q, int64_t q_st, int64_t q_sh, int64_t Tq, const void *k_nope, int64_t kn_st,
                     int64_t kn_sh, const void *k_pe, int64_t kp_st, const void *v, int64_t v_st, int64_t v_sh,
                     int64_t Tk, const int32_t *cu_q, const int32_t *cu_k, int B, int max_q, int H, float scale,

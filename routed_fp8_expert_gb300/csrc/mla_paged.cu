@@ -28,10 +28,13 @@ namespace {
 // of two tiles covers that if a tile's way through it stays short: arrival (2,800 cycles
 // from HBM under load), scores, softmax, first products. For the same reason the two
 // products have their issuing warps, and eight warps share a tile's softmax. 256 sequences
-// of 4,246 keys on average: 219 us, 5.9 TB/s of what has to be read and written. Keys that
-// many row tiles read come from L2, and shared memory is the bound: 240 KB that a tile's
+// of 4,246 keys on average: 217 us, 5.9 TB/s of what has to be read and written. The row
+// tiles of a sequence follow one another: where L2 still holds its keys by then (a chunk of
+// new tokens), shared memory is the bound; in a batch it does not, and HBM delivers them
+// once per row tile (64 sequences of 4,000 tokens, 128 heads: 579 MB read for a cache of
+// 295; 256 sequences 431 us for a floor of 207). Shared memory: 240 KB that a tile's
 // MMAs read and 80 KB that are written for them take 2,560 cycles of the 2,760 per tile
-// (512 new tokens over 7,000 keys: 945 us, 0.97 PFLOP/s).
+// (2 x 512 new tokens over 7,000 keys: 950 us, 0.96 PFLOP/s).
 //
 // The work is split evenly by key tiles over the CTAs, whatever the sequences' lengths:
 // the tiles of all (sequence, row tile) items form one line, CTA c takes the c-th part

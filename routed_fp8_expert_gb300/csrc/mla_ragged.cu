@@ -20,7 +20,8 @@ namespace {
 // Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each; P_t lies over the first half
 // of S_t (two 16-bit values per column). 2,560 tensor cycles per 256 x 128 scores bound a
 // long prompt, and the 336 KB that pass through shared memory for them take as long:
-// 8,192 tokens of 64 heads 860 us, 1.6 PFLOP/s (2,690 cycles at 128 bytes each). Short
+// 8,192 tokens of 64 heads 856 us, 1.6 PFLOP/s (2,690 cycles at 128 bytes each; 931 us at
+// the 1,830 MHz of the power limit). Short
 // prompts pay 8,000 cycles of start and end per CTA and the empty part of a sequence's
 // last 256 rows.
 constexpr int kTile = 128;

@@ -22,7 +22,7 @@ namespace {
 // are on their way before the angles are known; what only the key's warps need is theirs
 // alone, and with DIM, the rotary dimension when it is known at compile time (64, else 0),
 // the divisions by a head's vectors are shifts. 32 registers and CTAs of 128 threads keep
-// sixteen tokens on an SM: 8192 tokens of 64 heads 28.3 us, 5.4 TB/s (with 256 threads
+// sixteen tokens on an SM: 8192 tokens of 64 heads 27.8 us, 5.5 TB/s (with 256 threads
 // 31.3, without the two before 34.3; 27.3 for a dense copy of the queries' 134 MB alone),
 // of 16 heads 11.7 (16.5). Where an SM has no more than eight tokens, 256 threads have
 // each done sooner (1024 tokens of 16 heads 3.5 us, with 128 threads 4.1).

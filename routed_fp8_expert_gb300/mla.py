@@ -1,4 +1,4 @@
-"""Latent attention: the binding of the mla_* calls of include/moe_fp8.h.
+"""Latent attention: the binding of the mla_* calls of include/moe_fp8.h (forward only).
 
 Argument marshalling only, as in _lib: tensors on the CUDA device, bf16 or fp16, the
 innermost dimension contiguous; any other stride goes to the kernels as it is (views
